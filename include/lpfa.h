@@ -383,10 +383,207 @@ LPFA_API lpfa_status lpfa_attn_bwd_varlen(const uint8_t* q, const uint8_t* q_sf,
                                  int32_t output_mxfp8_dkv, void* stream);
 
 /*
+ * A (tokens, heads, 128) tensor with strides in elements: element (t, h, d) at
+ * ptr + t * tok_stride + h * head_stride + d.
+ */
+typedef struct {
+  void* ptr;
+  int64_t tok_stride;
+  int64_t head_stride;
+  int32_t heads;
+} lpfa_rows;
+
+typedef enum { LPFA_PAIR_INTERLEAVED = 0, LPFA_PAIR_HALF = 1 } lpfa_pairing;
+
+/*
+ * A rotation of the 64 element pairs of head_dim by positions on one or more axes (time, height
+ * and width of a patch; or one axis for text). Pair i is elements (2i, 2i + 1) or (i, i + 64) by
+ * `pairing`; it turns by position[axis[i]] * inv_freq[i] radians. inv_freq 0 leaves the pair as it
+ * is, so a head may be rotated in part.
+ */
+typedef struct {
+  int32_t axes;          /* columns of the position tensor, 1..8; every axis[i] is below it */
+  int32_t pairing;       /* lpfa_pairing */
+  double inv_freq[64];
+  uint8_t axis[64];
+} lpfa_rotary;
+
+/*
+ * What lpfa_qk_norm_rope and its relatives do to a row: the RMS norm, the weight, the rotation.
+ * The structure and the rotary it points to are host memory, read before the call returns.
+ */
+typedef struct {
+  const lpfa_rotary* rotary;  /* NULL: no rotation, positions are not read */
+  const void* positions;      /* device, (tokens, axes) int32 or int64, strides in elements */
+  int64_t pos_tok_stride;
+  int64_t pos_axis_stride;
+  int32_t pos_int64;          /* 1: int64 positions, 0: int32 */
+  int32_t norm;               /* 1: divide by sqrt(mean(x^2) + eps), 0: no norm */
+  float eps;                  /* >= 0, finite */
+  const void* q_weight;       /* device, one row of 128 (head stride 0) or a row per head; NULL: 1 */
+  int64_t q_weight_head_stride;
+  const void* k_weight;
+  int64_t k_weight_head_stride;
+  lpfa_in_dtype weight_dtype; /* of both weights */
+} lpfa_norm_rope;
+
+/*
+ * Per-head norm and rotary positions of Q and K in one pass, the step before the quantizer (or
+ * before a BF16 attention): for every row x of 128 (token t, head h),
+ *   u = x * rsqrt(mean(x^2) + eps) * weight,   (a, b) -> (a cos - b sin, a sin + b cos)
+ * with the angle of (token, pair) as lpfa_rotary says. Everything is FP32 (angles FP64) and rounded
+ * once, to the output type.
+ *
+ * q, k         inputs of dtype dt; k NULL (or k->heads 0): Q alone. Head counts may differ.
+ * q_out, k_out outputs of dtype out_dt with the heads of q, k. An output may be its own input
+ *              (the same ptr, strides and dtype); otherwise outputs overlap nothing.
+ * Alignment:   every ptr 16-byte aligned with strides multiples of 8 (bf16) or 4 (fp32) elements,
+ *              weights likewise.
+ * Errors:      LPFA_ERR_INVALID_ARG for NULL pointers, tokens < 1, head_dim != 128, more than 1024
+ *              heads in all, bad enums, an eps or frequency that is not finite, an axis outside the
+ *              positions' columns, or misalignment; LPFA_ERR_UNSUPPORTED off sm_100; LPFA_ERR_CUDA
+ *              on launch failure.
+ */
+LPFA_API lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
+                                       int64_t tokens, int32_t head_dim, const lpfa_norm_rope* op,
+                                       const lpfa_rows* q_out, const lpfa_rows* k_out,
+                                       lpfa_in_dtype out_dt, void* stream);
+
+/*
+ * lpfa_qk_norm_rope straight into MXFP8: the FP32 results go through the quantizer's rule
+ * (lpfa_quantize_mxfp8_varlen, head_dim orientation) without a rounding in between, so the bytes
+ * are those of lpfa_qk_norm_rope with FP32 outputs followed by the quantizer. Results must be finite.
+ *
+ * meta                     describes the tokens of q and k alike (its total is their count).
+ * q_payload, k_payload     device, (T, heads, 128) E4M3 codes, contiguous.
+ * q_scales, k_scales       device, lpfa_scale_bytes(meta, heads) bytes each.
+ * Other arguments, alignment and errors as for lpfa_qk_norm_rope and the quantizer.
+ */
+LPFA_API lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
+                                             int32_t head_dim, const lpfa_varlen_meta* meta,
+                                             const lpfa_norm_rope* op, lpfa_scaling_mode mode,
+                                             uint8_t* q_payload, uint8_t* q_scales,
+                                             uint8_t* k_payload, uint8_t* k_scales, void* stream);
+
+/*
+ * Gradients of lpfa_qk_norm_rope. With g the incoming gradient turned back by the pair's angle,
+ * r = rsqrt(mean(x^2) + eps) (1 without the norm) and h = g * weight:
+ *   dweight = sum over tokens (and heads, for one row of weights) of g * x * r,
+ *   dx = r * h - x * r^3 * mean(h * x)   (without the norm: h).
+ * The norm is recomputed from x; nothing of the forward is kept.
+ *
+ * dq_out, dk_out       gradients of the outputs, dtype dt (dk_out NULL or 0 heads: Q alone).
+ * q, k                 the forward's inputs, dtype dt.
+ * dq, dk               outputs of dtype dt; each may be its own dq_out / dk_out (same ptr, strides).
+ * dq_weight, dk_weight device, fp32 outputs of the weight's rows, contiguous (128 or heads * 128
+ *                      values); required where op has that weight.
+ * workspace            device, 16-byte aligned, at least lpfa_qk_norm_rope_bwd_workspace_bytes bytes,
+ *                      owned by the caller, written by the call and free again once its work has
+ *                      finished. May be NULL where op has no weight.
+ * Sums are taken in a fixed order: equal calls give equal bits. Errors as for lpfa_qk_norm_rope.
+ */
+LPFA_API size_t lpfa_qk_norm_rope_bwd_workspace_bytes(int32_t q_heads, int32_t k_heads,
+                                                      const lpfa_norm_rope* op);
+LPFA_API lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_out,
+                                           const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
+                                           int64_t tokens, int32_t head_dim, const lpfa_norm_rope* op,
+                                           const lpfa_rows* dq, const lpfa_rows* dk, float* dq_weight,
+                                           float* dk_weight, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/*
+ * A paged key/value cache in MXFP4: E2M1 codes with one E8M0 scale per 32 elements along head_dim,
+ * 17/32 byte per element, the quantizer's block format at four bits.
+ *
+ * k, v         device, (num_pages, heads, page_size, 64) bytes: element 32 b + 4 g + 2 j + n of a
+ *              row (b < 4, g < 8, j < 2) is the low (n = 0) or high (n = 1) nibble of byte
+ *              8 g + 2 b + j.
+ * k_sf, v_sf   device, (num_pages, heads, page_size, 4) scale bytes, e + 127 for the power 2^e.
+ * page_size    tokens per page: 16, 32, 64, 128 or 256.
+ * All four 16-byte aligned. Rules of the codes: RCEIL: the smallest e with amax <= 6 * 2^e; FLOOR:
+ * floor(log2 amax) - 2; e clamped to [-127, 127]; amax 0 gives byte 0. Code = E2M1(x * 2^-e), round
+ * to nearest even, saturating to +-6, sign kept.
+ */
+typedef struct {
+  uint8_t* k;
+  uint8_t* k_sf;
+  uint8_t* v;
+  uint8_t* v_sf;
+  int32_t num_pages;
+  int32_t heads;
+  int32_t page_size;
+} lpfa_kv4_cache;
+
+/*
+ * Which page holds which tokens: token p of sequence s is row p % page_size of page
+ * ptr[s * seq_stride + p / page_size], p / page_size < width. Entries that no token needs may hold
+ * anything. A needed entry outside [0, num_pages), or a token beyond the table, is skipped by the
+ * kernels, never followed: the token is not written, reads as zeros, or is not attended to, and
+ * LPFA_ERR_INVALID_ARG is recorded in the device status word.
+ */
+typedef struct {
+  const int32_t* ptr;   /* device */
+  int64_t seq_stride;
+  int32_t width;        /* width * page_size <= 2^30 */
+} lpfa_page_table;
+
+/*
+ * Append: quantize the packed new tokens of K and V into the cache. Token j of sequence i (under
+ * meta) becomes cached token start[i] + j. Nothing else in the cache is touched.
+ *
+ * k, v      device, (T, heads, 128) of dtype dt with the cache's heads, strides as for the quantizer.
+ *           Values must be finite.
+ * start     device, int32 per sequence: tokens cached before; NULL: 0.
+ * Two tokens of one call must not share a slot (two sequences whose tables name the same page for
+ * new tokens): such a slot holds a mixture. Errors: LPFA_ERR_INVALID_ARG for NULL pointers,
+ * head_dim != 128, heads that differ from the cache's, a bad page size, enum, width or meta, or
+ * misalignment; LPFA_ERR_UNSUPPORTED off sm_100; LPFA_ERR_CUDA on launch failure.
+ */
+LPFA_API lpfa_status lpfa_kv4_write(const lpfa_rows* k, const lpfa_rows* v, lpfa_in_dtype dt,
+                                    int32_t head_dim, const lpfa_kv4_cache* cache,
+                                    const lpfa_page_table* table, const int32_t* start,
+                                    const lpfa_varlen_meta* meta, lpfa_scaling_mode mode, void* stream);
+
+/*
+ * The cached tokens start[i] .. start[i] + len_i of each sequence (len_i from meta) as packed MXFP8
+ * tensors in the quantizer's layout, exactly: E2M1 codes are E4M3 values and the scales are the
+ * same bytes. For a long chunk of queries over a cached prefix, through lpfa_attn_fwd_varlen (bf16
+ * PV mode) or lpfa_dequantize_mxfp8_varlen. Rows past a sequence's end get scale bytes 0x7F.
+ * Errors as for lpfa_kv4_write.
+ */
+LPFA_API lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* table,
+                                   const int32_t* start, const lpfa_varlen_meta* meta, int32_t head_dim,
+                                   uint8_t* k_payload, uint8_t* k_scales, uint8_t* v_payload,
+                                   uint8_t* v_scales, void* stream);
+
+/*
+ * Attention of a few query tokens per sequence over the MXFP4 cache (decoding; drafted tokens),
+ * head-dim 128, q_heads a multiple of the cache's heads (query head h reads key head
+ * h / (q_heads / heads)). Scale 1 / sqrt(128); P is rounded to FP16, the codes are exact, sums and
+ * softmax statistics are FP32. Any number of query tokens is right; the kernel reads the cache once
+ * per 16 query rows, so long chunks are faster through lpfa_kv4_read and lpfa_attn_fwd_varlen.
+ *
+ * q          bf16 rows (Tq, q_heads, 128) under meta_q, strides in elements.
+ * kv_lens    device, int32 per sequence: cached tokens, those of this step included; 0 is allowed.
+ *            A negative one counts as 0 and one beyond the table as the table's room; both are
+ *            recorded in the device status word as LPFA_ERR_INVALID_ARG.
+ * causal     0: every query sees all kv_lens[i] keys. 1: query token j of L sees the first
+ *            kv_lens[i] - L + j + 1 (the queries are the sequence's last tokens).
+ * out_bf16   device, (Tq, q_heads, 128) bf16, contiguous. A row that sees no key is 0.
+ * lse        device, (q_heads, Tq) fp32, natural log; -inf for a row that sees no key.
+ * A K scale byte of 0 counts as 0. Equal calls give equal bits. Errors as for lpfa_kv4_write.
+ */
+LPFA_API lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_kv4_cache* cache,
+                                       const lpfa_page_table* table, const int32_t* kv_lens,
+                                       const lpfa_varlen_meta* meta_q, int32_t causal, void* out_bf16,
+                                       float* lse, void* stream);
+
+/*
  * Device status word. Kernels that bound their barrier waits record a failure code in a
  * library-owned device word instead of hanging. This call synchronizes `stream`, reads the
- * word of the current device, resets it to zero, and returns LPFA_OK, LPFA_ERR_TIMEOUT, or
- * LPFA_ERR_CUDA if the synchronization itself failed. *detail (may be NULL) receives the
+ * word of the current device, resets it to zero, and returns LPFA_OK, LPFA_ERR_TIMEOUT,
+ * LPFA_ERR_INVALID_ARG (a length, start or page table entry in device memory that a kernel found
+ * out of range: sites 300 to 303) or LPFA_ERR_CUDA if the synchronization itself failed. *detail (may be NULL) receives the
  * recorded diagnostic (which wait gave up), 0 if none.
  *
  * There is one such word per device and process, shared by every kernel of this library and

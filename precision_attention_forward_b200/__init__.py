@@ -41,7 +41,9 @@ EXPORTED_SYMBOLS = (
     "lpfa_attn_fwd_varlen_descaled", "lpfa_quantize_mxfp8_varlen_tokens", "lpfa_attn_bwd_varlen",
     "lpfa_attn_bwd_varlen_debug", "lpfa_attn_fwd_shared_q", "lpfa_dequantize_mxfp8_varlen",
     "lpfa_attn_fwd_workspace_bytes", "lpfa_attn_fwd_varlen_ws", "lpfa_attn_fwd_shared_q_ws",
-    "lpfa_attn_fwd_varlen_noalloc",
+    "lpfa_attn_fwd_varlen_noalloc", "lpfa_qk_norm_rope", "lpfa_qk_norm_rope_mxfp8",
+    "lpfa_qk_norm_rope_bwd_workspace_bytes", "lpfa_qk_norm_rope_bwd", "lpfa_kv4_write", "lpfa_kv4_read",
+    "lpfa_attn_fwd_kv4",
 )
 
 
@@ -59,6 +61,33 @@ class _Meta(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
                 ("total_scale_blocks", ctypes.c_int32), ("max_seqlen", ctypes.c_int32),
                 ("dev", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("pairing", ctypes.c_int32), ("inv_freq", ctypes.c_double * 64),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
+class _NormRope(ctypes.Structure):
+    _fields_ = [("rotary", ctypes.POINTER(_Rotary)), ("positions", ctypes.c_void_p), ("pos_tok_stride", ctypes.c_int64),
+                ("pos_axis_stride", ctypes.c_int64), ("pos_int64", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("q_weight_head_stride", ctypes.c_int64),
+                ("k_weight", ctypes.c_void_p), ("k_weight_head_stride", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int)]
+
+
+class _Kv4Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_sf", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_sf", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("width", ctypes.c_int32)]
 
 
 _vp, _i32, _i64, _f32p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
@@ -103,6 +132,26 @@ _lib.lpfa_attn_fwd_workspace_bytes.argtypes = [ctypes.POINTER(_Meta), _i32, ctyp
 _lib.lpfa_attn_fwd_workspace_bytes.restype = ctypes.c_size_t
 _lib.lpfa_dequantize_mxfp8_varlen.argtypes = [_vp, _vp, ctypes.POINTER(_Meta), _i32, _i32, _vp, _vp]
 _lib.lpfa_dequantize_mxfp8_varlen.restype = ctypes.c_int
+_rows_p, _op_p = ctypes.POINTER(_Rows), ctypes.POINTER(_NormRope)
+_lib.lpfa_qk_norm_rope.argtypes = [_rows_p, _rows_p, ctypes.c_int, _i64, _i32, _op_p, _rows_p, _rows_p, ctypes.c_int,
+                                   _vp]
+_lib.lpfa_qk_norm_rope.restype = ctypes.c_int
+_lib.lpfa_qk_norm_rope_mxfp8.argtypes = [_rows_p, _rows_p, ctypes.c_int, _i32, ctypes.POINTER(_Meta), _op_p,
+                                         ctypes.c_int, _vp, _vp, _vp, _vp, _vp]
+_lib.lpfa_qk_norm_rope_mxfp8.restype = ctypes.c_int
+_lib.lpfa_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i32, _i32, _op_p]
+_lib.lpfa_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+_lib.lpfa_qk_norm_rope_bwd.argtypes = ([_rows_p] * 4 + [ctypes.c_int, _i64, _i32, _op_p, _rows_p, _rows_p, _vp, _vp,
+                                                        _vp, ctypes.c_size_t, _vp])
+_lib.lpfa_qk_norm_rope_bwd.restype = ctypes.c_int
+_cache_p, _table_p = ctypes.POINTER(_Kv4Cache), ctypes.POINTER(_PageTable)
+_lib.lpfa_kv4_write.argtypes = [_rows_p, _rows_p, ctypes.c_int, _i32, _cache_p, _table_p, _vp, ctypes.POINTER(_Meta),
+                                ctypes.c_int, _vp]
+_lib.lpfa_kv4_write.restype = ctypes.c_int
+_lib.lpfa_kv4_read.argtypes = [_cache_p, _table_p, _vp, ctypes.POINTER(_Meta), _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.lpfa_kv4_read.restype = ctypes.c_int
+_lib.lpfa_attn_fwd_kv4.argtypes = [_rows_p, _i32, _cache_p, _table_p, _vp, ctypes.POINTER(_Meta), _i32, _vp, _vp, _vp]
+_lib.lpfa_attn_fwd_kv4.restype = ctypes.c_int
 _lib.lpfa_device_status.argtypes = [_vp, ctypes.POINTER(_i32)]
 _lib.lpfa_device_status.restype = ctypes.c_int
 _lib.lpfa_last_error_message.argtypes = []
@@ -453,6 +502,444 @@ def lpfa_attn_bwd_varlen(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor, k
     if output_mxfp8_dkv:
         return dq, dk, dv, dk_sf, dv_sf
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------------------
+# Norm and rotation of Q and K
+# ---------------------------------------------------------------------------------------
+_DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}
+PAIRINGS = {"interleaved": 0, "half": 1}
+
+
+class _Scope:
+    """The device and stream of one call. Buffers made inside belong to the stream that the call's
+    work runs on (its allocator pool), so neither earlier nor later work of another stream can share
+    their memory; `seen_by_caller` marks results that the caller's own stream will go on to read."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.restore = None
+        index = device.index
+        if index is not None and index != torch.cuda.current_device():
+            self.restore = torch.cuda.device(device)
+        self.other = None
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.other = stream
+        self.stream = stream
+
+    def __enter__(self):
+        if self.restore is not None:
+            self.restore.__enter__()
+        self.caller = torch.cuda.current_stream()
+        if self.other is None or self.other.cuda_stream == self.caller.cuda_stream:
+            self.other = None
+            self.handle = self.caller.cuda_stream
+        else:
+            self.handle = self.other.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.restore is not None:
+            self.restore.__exit__(*exc)
+
+    def empty(self, shape, dtype, seen_by_caller=True):
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        if seen_by_caller:
+            t.record_stream(self.caller)
+        return t
+
+
+def _rows(t: Optional[torch.Tensor], name: str, dtype=None, device=None, shape=None) -> Optional[_Rows]:
+    """A (tokens, heads, 128) tensor as an lpfa_rows; None stays None."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.shape[2] != 128 or t.stride(2) != 1 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise ValueError("%s must be a (tokens, heads, 128) tensor with a contiguous last dimension" % name)
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError("%s must be on the CUDA device of the other tensors" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    if t.dtype not in _DTYPE_CODE:
+        raise ValueError("%s must be bf16 or fp32" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    # The stride of an axis of one element is never stepped over; it may be anything.
+    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * 128,
+                 t.stride(1) if t.shape[1] > 1 else 128, t.shape[1])
+
+
+def _out_rows(t: torch.Tensor, name: str, dtype, device, shape) -> _Rows:
+    """As _rows, for a tensor that is written: its elements must be different memory."""
+    r = _rows(t, name, dtype, device, shape)
+    lo, hi = sorted(((r.tok_stride, t.shape[0]), (r.head_stride, t.shape[1])))
+    if (lo[0] < 128 and lo[1] > 1) or (hi[1] > 1 and hi[0] < (lo[0] * (lo[1] - 1) + 128 if lo[1] > 1 else 128)):
+        raise ValueError("%s has rows that overlap" % name)
+    return r
+
+
+def _contiguous(t: torch.Tensor, name: str, dtype, device, shape) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the device of the others"
+                         % (name, dtype, tuple(shape)))
+    return t
+
+
+class RotaryAxes:
+    """How positions on one or more axes turn the 64 element pairs of a head.
+
+    dims        head_dim elements given to each axis, even numbers with a sum of at most 128, e.g.
+                (44, 42, 42) for time, height and width, or (128,) for text. Axis a owns the next
+                dims[a] / 2 pairs, pair j of them with frequency theta[a] ** (-2 j / dims[a]). Pairs
+                that no axis owns are left as they are.
+    theta       one base for all axes, or one for each.
+    pairing     "interleaved": pair i is elements (2i, 2i + 1); "half": (i, i + 64).
+
+    from_frequencies takes any frequency and axis for each pair (scaled or shared spectra).
+    """
+
+    def __init__(self, dims: Sequence[int] = (128,), theta=10000.0, pairing: str = "interleaved"):
+        dims = [int(d) for d in dims]
+        thetas = [float(theta)] * len(dims) if np.ndim(theta) == 0 else [float(x) for x in theta]
+        if not dims or any(d < 0 or d % 2 for d in dims) or sum(dims) > 128 or len(thetas) != len(dims):
+            raise ValueError("dims must be even, sum to at most 128 and have one theta each (or one for all)")
+        if any(not (x > 0) for x in thetas):
+            raise ValueError("theta must be positive")
+        freq, axis = [], []
+        for a, (d, base) in enumerate(zip(dims, thetas)):
+            for j in range(d // 2):
+                freq.append(base ** (-2.0 * j / d))
+                axis.append(a)
+        freq += [0.0] * (64 - len(freq))
+        axis += [0] * (64 - len(axis))
+        self._fill(freq, axis, len(dims), pairing)
+
+    @classmethod
+    def from_frequencies(cls, inv_freq: Sequence[float], axis: Optional[Sequence[int]] = None,
+                         pairing: str = "interleaved") -> "RotaryAxes":
+        """inv_freq: radians per position step of each of the 64 pairs; axis: its position column (0)."""
+        freq = [float(x) for x in inv_freq]
+        ax = [0] * 64 if axis is None else [int(x) for x in axis]
+        if len(freq) != 64 or len(ax) != 64 or min(ax) < 0:
+            raise ValueError("a head has 64 pairs: give 64 frequencies and axes")
+        self = cls.__new__(cls)
+        self._fill(freq, ax, max(ax) + 1, pairing)
+        return self
+
+    def _fill(self, freq, axis, axes, pairing):
+        if pairing not in PAIRINGS:
+            raise ValueError("pairing must be 'interleaved' or 'half'")
+        if not 1 <= axes <= 8:
+            raise ValueError("a rotation has 1 to 8 axes")
+        if not np.isfinite(freq).all():
+            raise ValueError("frequencies must be finite")
+        self.axes, self.pairing = axes, pairing
+        self.inv_freq, self.axis = tuple(freq), tuple(axis)
+        self._c = _Rotary(axes, PAIRINGS[pairing], (ctypes.c_double * 64)(*freq), (ctypes.c_uint8 * 64)(*axis))
+
+
+def _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm) -> _NormRope:
+    op = _NormRope()
+    op.norm = 1 if norm else 0
+    op.eps = eps
+    if norm and not (0.0 <= eps < float("inf")):
+        raise ValueError("eps must be finite and >= 0")
+    if rope is not None:
+        if not isinstance(rope, RotaryAxes):
+            raise ValueError("rope must be a RotaryAxes or None")
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        pos = positions.unsqueeze(1) if positions.dim() == 1 else positions
+        if pos.dim() != 2 or pos.shape[0] != q.shape[0] or pos.shape[1] < rope.axes:
+            raise ValueError("positions must be (tokens, axes): %d tokens, %d axes" % (q.shape[0], rope.axes))
+        if pos.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be int32 or int64")
+        if pos.device != q.device:
+            raise ValueError("positions must be on the device of q")
+        op.rotary = ctypes.pointer(rope._c)
+        op.positions = pos.data_ptr()
+        op.pos_tok_stride, op.pos_axis_stride = pos.stride(0), pos.stride(1)
+        op.pos_int64 = 1 if pos.dtype == torch.int64 else 0
+    wdt = None
+    for name, x, w in (("q", q, q_weight), ("k", k, k_weight)):
+        if w is None:
+            continue
+        if x is None:
+            raise ValueError("k_weight without k")
+        if w.dtype not in _DTYPE_CODE or (wdt is not None and w.dtype != wdt):
+            raise ValueError("weights must be bf16 or fp32, both the same")
+        if tuple(w.shape) not in ((128,), (x.shape[1], 128)) or not w.is_contiguous() or w.device != q.device:
+            raise ValueError("%s_weight must be a contiguous (128,) or (heads, 128) tensor on the device of q" % name)
+        wdt = w.dtype
+        stride = 128 if w.dim() == 2 else 0
+        if name == "q":
+            op.q_weight, op.q_weight_head_stride = w.data_ptr(), stride
+        else:
+            op.k_weight, op.k_weight_head_stride = w.data_ptr(), stride
+    op.weight_dtype = _DTYPE_CODE[wdt] if wdt is not None else 0
+    return op
+
+
+def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                      rope: Optional[RotaryAxes], q_weight: Optional[torch.Tensor] = None,
+                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, norm: bool = True,
+                      out_dtype: Optional[torch.dtype] = None, q_out: Optional[torch.Tensor] = None,
+                      k_out: Optional[torch.Tensor] = None, stream=None):
+    """Per-head RMS norm and rotary positions of Q and K in one launch; returns (q_out, k_out).
+
+    q, k: (tokens, heads, 128) bf16 or fp32 with any strides (views of a joint projection included);
+    their head counts may differ and k may be None. positions: (tokens, axes) int32 or int64, or
+    (tokens,) for one axis. rope: a RotaryAxes, or None for no rotation. q_weight, k_weight: (128,) or
+    (heads, 128), bf16 or fp32. norm=False leaves the norm out (the weight still applies).
+    Outputs: out_dtype (the input's by default), contiguous unless given; an output may be its own input.
+    """
+    qr = _rows(q, "q")
+    device, dt = q.device, q.dtype
+    kr = _rows(k, "k", dt, device)
+    if k is not None and k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must have the same tokens")
+    odt = dt if out_dtype is None else out_dtype
+    if odt not in _DTYPE_CODE:
+        raise ValueError("out_dtype must be bf16 or fp32")
+    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    with _Scope(device, stream) as sc:
+        if q_out is None:
+            q_out = sc.empty(q.shape, odt)
+        qo = _out_rows(q_out, "q_out", odt, device, q.shape)
+        ko = None
+        if k is not None:
+            if k_out is None:
+                k_out = sc.empty(k.shape, odt)
+            ko = _out_rows(k_out, "k_out", odt, device, k.shape)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        _check(_lib.lpfa_qk_norm_rope(qr, kr, _DTYPE_CODE[dt], q.shape[0], 128, op, qo, ko, _DTYPE_CODE[odt], sc.handle))
+    return q_out, k_out
+
+
+def lpfa_qk_norm_rope_mxfp8(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                            rope: Optional[RotaryAxes], meta: VarlenMeta, q_weight: Optional[torch.Tensor] = None,
+                            k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, norm: bool = True,
+                            scaling_mode: str = "rceil", q_payload: Optional[torch.Tensor] = None,
+                            q_scales: Optional[torch.Tensor] = None, k_payload: Optional[torch.Tensor] = None,
+                            k_scales: Optional[torch.Tensor] = None, stream=None):
+    """lpfa_qk_norm_rope straight into the attention's input: returns (q_payload, q_scales, k_payload,
+    k_scales) as lpfa_quantize_mxfp8_varlen lays them out (None for k without k). The bytes are those
+    of lpfa_qk_norm_rope with fp32 outputs and the quantizer after it."""
+    qr = _rows(q, "q")
+    device, dt = q.device, q.dtype
+    kr = _rows(k, "k", dt, device)
+    if k is not None and k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must have the same tokens")
+    if q.shape[0] != meta.total_tokens:
+        raise ValueError("q has %d tokens but the metadata describes %d" % (q.shape[0], meta.total_tokens))
+    if scaling_mode not in SCALING_MODES:
+        raise ValueError("scaling_mode must be 'rceil' or 'floor'")
+    _check_meta_device(meta, device)
+    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    with _Scope(device, stream) as sc:
+        outs = []
+        for x, payload, scales, name in ((q, q_payload, q_scales, "q"), (k, k_payload, k_scales, "k")):
+            if x is None:
+                if payload is not None or scales is not None:
+                    raise ValueError("k_payload or k_scales without k")
+                outs += [None, None]
+                continue
+            T, H = x.shape[0], x.shape[1]
+            nb = (meta.scale_bytes(H),)
+            outs.append(sc.empty((T, H, 128), torch.uint8) if payload is None else
+                        _contiguous(payload, name + "_payload", torch.uint8, device, (T, H, 128)))
+            outs.append(sc.empty(nb, torch.uint8) if scales is None else
+                        _contiguous(scales, name + "_scales", torch.uint8, device, nb))
+        _check(_lib.lpfa_qk_norm_rope_mxfp8(qr, kr, _DTYPE_CODE[dt], 128, meta._c, op, SCALING_MODES[scaling_mode],
+                                            *[_ptr(x) for x in outs], sc.handle))
+    return tuple(outs)
+
+
+def lpfa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                          k: Optional[torch.Tensor], positions: Optional[torch.Tensor], rope: Optional[RotaryAxes],
+                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, norm: bool = True, dq: Optional[torch.Tensor] = None,
+                          dk: Optional[torch.Tensor] = None, dq_weight: Optional[torch.Tensor] = None,
+                          dk_weight: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of lpfa_qk_norm_rope: returns (dq, dk, dq_weight, dk_weight), None for what is absent.
+
+    dq_out, dk_out: gradients of its outputs, in the inputs' dtype (the attention backward's dQ and dK
+    for bf16); q, k and the rest as in the forward call. Weight gradients are fp32 in the weight's
+    shape. dq may be dq_out's memory, dk dk_out's. Equal calls give equal bits.
+    """
+    qr = _rows(q, "q")
+    device, dt = q.device, q.dtype
+    kr = _rows(k, "k", dt, device)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out come together")
+    if k is not None and k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must have the same tokens")
+    gq = _rows(dq_out, "dq_out", dt, device, q.shape)
+    gk = _rows(dk_out, "dk_out", dt, device, k.shape) if k is not None else None
+    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    with _Scope(device, stream) as sc:
+        dq = sc.empty(q.shape, dt) if dq is None else dq
+        dqr = _out_rows(dq, "dq", dt, device, q.shape)
+        dkr = None
+        if k is not None:
+            dk = sc.empty(k.shape, dt) if dk is None else dk
+            dkr = _out_rows(dk, "dk", dt, device, k.shape)
+        elif dk is not None:
+            raise ValueError("dk without k")
+        dws = []
+        for w, dw, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+            if w is None:
+                if dw is not None:
+                    raise ValueError("%s without its weight" % name)
+                dws.append(None)
+            else:
+                dws.append(sc.empty(w.shape, torch.float32) if dw is None else
+                           _contiguous(dw, name, torch.float32, device, w.shape))
+        need = _lib.lpfa_qk_norm_rope_bwd_workspace_bytes(q.shape[1], 0 if k is None else k.shape[1], op)
+        ws = sc.empty((need,), torch.uint8, seen_by_caller=False) if need else None
+        _check(_lib.lpfa_qk_norm_rope_bwd(gq, gk, qr, kr, _DTYPE_CODE[dt], q.shape[0], 128, op, dqr, dkr, _ptr(dws[0]),
+                                          _ptr(dws[1]), _ptr(ws), need, sc.handle))
+    return dq, dk, dws[0], dws[1]
+
+
+# ---------------------------------------------------------------------------------------
+# MXFP4 key/value cache
+# ---------------------------------------------------------------------------------------
+def _check_meta_device(meta: VarlenMeta, device) -> None:
+    if meta.dev is None or meta.dev.device != device:
+        raise ValueError("the metadata must have a device buffer on the device of the tensors")
+
+
+class Kv4Cache:
+    """Pages of K and V in MXFP4 (include/lpfa.h, lpfa_kv4_cache): k and v are (num_pages, heads,
+    page_size, 64) uint8, k_scales and v_scales (num_pages, heads, page_size, 4) uint8. Which page
+    belongs to whom is the caller's page table; a page is copied, shared or freed by index."""
+
+    def __init__(self, num_pages: int, heads: int, page_size: int = 64, device="cuda"):
+        if num_pages < 1 or heads < 1 or page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("a cache has pages and heads, and 16, 32, 64, 128 or 256 tokens per page")
+        shape = (num_pages, heads, page_size)
+        self._set(*[torch.zeros(shape + (n,), dtype=torch.uint8, device=device) for n in (64, 4, 64, 4)])
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, k_scales: torch.Tensor, v: torch.Tensor, v_scales: torch.Tensor) -> "Kv4Cache":
+        """A cache over existing tensors of the shapes above (a server's own pool)."""
+        self = cls.__new__(cls)
+        self._set(k, k_scales, v, v_scales)
+        return self
+
+    def _set(self, k, k_scales, v, v_scales):
+        if k.dim() != 4 or k.shape[3] != 64 or k.shape[2] not in (16, 32, 64, 128, 256):
+            raise ValueError("k must be (num_pages, heads, page_size, 64) with 16, 32, 64, 128 or 256 tokens per page")
+        if k.device.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
+        for name, t, n in (("k", k, 64), ("k_scales", k_scales, 4), ("v", v, 64), ("v_scales", v_scales, 4)):
+            _contiguous(t, name, torch.uint8, k.device, tuple(k.shape[:3]) + (n,))
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self.num_pages, self.heads, self.page_size = k.shape[0], k.shape[1], k.shape[2]
+        self.device = k.device
+        self._c = _Kv4Cache(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), *k.shape[:3])
+
+
+def _page_table(page_table: torch.Tensor, num_seqs: int, device) -> _PageTable:
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != num_seqs or
+            page_table.shape[1] < 1 or (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
+        raise ValueError("page_table must be an int32 (sequences, pages) tensor with contiguous rows: %d sequences"
+                         % num_seqs)
+    if page_table.device != device:
+        raise ValueError("page_table must be on the device of the cache")
+    return _PageTable(page_table.data_ptr(), page_table.stride(0), page_table.shape[1])
+
+
+def _seq_ints(t: Optional[torch.Tensor], name: str, num_seqs: int, device) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != (num_seqs,) or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous int32 tensor of %d sequences on the device of the cache" % (name, num_seqs))
+    return t.data_ptr()
+
+
+def lpfa_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta,
+                   start: Optional[torch.Tensor] = None, scaling_mode: str = "rceil", stream=None) -> None:
+    """Quantize the packed new tokens k, v (T, heads, 128) (bf16 or fp32) into the cache's pages.
+
+    meta: the new tokens of each sequence; start: int32 tokens cached before (None: 0); page_table:
+    int32 (sequences, pages), token p of sequence s is row p % page_size of page
+    page_table[s, p // page_size]. A page index out of range, or a token beyond the table, is skipped
+    and reported by lpfa_device_status. Two tokens of a call must not share a slot.
+    """
+    device = cache.device
+    kr = _rows(k, "k", None, device)
+    vr = _rows(v, "v", k.dtype, device, k.shape)
+    if k.shape[1] != cache.heads:
+        raise ValueError("k has %d heads, the cache %d" % (k.shape[1], cache.heads))
+    if k.shape[0] != meta.total_tokens:
+        raise ValueError("k has %d tokens but the metadata describes %d" % (k.shape[0], meta.total_tokens))
+    if scaling_mode not in SCALING_MODES:
+        raise ValueError("scaling_mode must be 'rceil' or 'floor'")
+    _check_meta_device(meta, device)
+    table = _page_table(page_table, meta.num_seqs, device)
+    starts = _seq_ints(start, "start", meta.num_seqs, device)
+    with _Scope(device, stream) as sc:
+        _check(_lib.lpfa_kv4_write(kr, vr, _DTYPE_CODE[k.dtype], 128, cache._c, table, starts, meta._c,
+                                   SCALING_MODES[scaling_mode], sc.handle))
+
+
+def lpfa_kv4_read(cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta, start: Optional[torch.Tensor] = None,
+                  k_payload: Optional[torch.Tensor] = None, k_scales: Optional[torch.Tensor] = None,
+                  v_payload: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None, stream=None):
+    """The cached tokens start[i] .. start[i] + length_i (lengths from meta) as packed MXFP8 tensors,
+    exactly: (k_payload, k_scales, v_payload, v_scales) in the quantizer's layout, for
+    lpfa_attn_fwd_varlen (pv_mode "bf16") or lpfa_dequantize_mxfp8_varlen."""
+    device = cache.device
+    _check_meta_device(meta, device)
+    table = _page_table(page_table, meta.num_seqs, device)
+    starts = _seq_ints(start, "start", meta.num_seqs, device)
+    T, H = meta.total_tokens, cache.heads
+    nb = meta.scale_bytes(H)
+    with _Scope(device, stream) as sc:
+        outs = []
+        for t, name, shape in ((k_payload, "k_payload", (T, H, 128)), (k_scales, "k_scales", (nb,)),
+                               (v_payload, "v_payload", (T, H, 128)), (v_scales, "v_scales", (nb,))):
+            outs.append(sc.empty(shape, torch.uint8) if t is None else _contiguous(t, name, torch.uint8, device, shape))
+        _check(_lib.lpfa_kv4_read(cache._c, table, starts, meta._c, 128, *[t.data_ptr() for t in outs], sc.handle))
+    return tuple(outs)
+
+
+def lpfa_attn_fwd_kv4(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                      meta_q: VarlenMeta, causal: bool = False, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a few query tokens per sequence over the MXFP4 cache; returns (out bf16
+    (Tq, q_heads, 128), lse fp32 (q_heads, Tq)).
+
+    q: bf16 (Tq, q_heads, 128), q_heads a multiple of the cache's heads, packed under meta_q. kv_lens:
+    int32 per sequence, the cached tokens (this step's included; 0 gives O = 0, LSE = -inf). causal:
+    query token j of L sees the first kv_lens - L + j + 1 keys, else all of them. The page table is as
+    for lpfa_kv4_write. For chunks of many query tokens, lpfa_kv4_read and lpfa_attn_fwd_varlen are faster.
+    """
+    device = cache.device
+    qr = _rows(q, "q", torch.bfloat16, device)
+    Tq, H = q.shape[0], q.shape[1]
+    if H % cache.heads:
+        raise ValueError("%d query heads are not a multiple of the cache's %d" % (H, cache.heads))
+    if Tq != meta_q.total_tokens:
+        raise ValueError("q has %d tokens but the metadata describes %d" % (Tq, meta_q.total_tokens))
+    _check_meta_device(meta_q, device)
+    table = _page_table(page_table, meta_q.num_seqs, device)
+    if kv_lens is None:
+        raise ValueError("kv_lens is needed")
+    lens = _seq_ints(kv_lens, "kv_lens", meta_q.num_seqs, device)
+    with _Scope(device, stream) as sc:
+        out = sc.empty((Tq, H, 128), torch.bfloat16) if out is None else _contiguous(out, "out", torch.bfloat16, device, (Tq, H, 128))
+        lse = sc.empty((H, Tq), torch.float32) if lse is None else _contiguous(lse, "lse", torch.float32, device, (H, Tq))
+        _check(_lib.lpfa_attn_fwd_kv4(qr, 128, cache._c, table, lens, meta_q._c, 1 if causal else 0, out.data_ptr(),
+                                      lse.data_ptr(), sc.handle))
+    return out, lse
 
 
 def lpfa_device_status(stream=None):

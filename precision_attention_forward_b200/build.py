@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "liblpfa.so")
 
 SOURCES = ["lpfa.cu"]
-HEADERS = ["ptx.cuh", "quantize.cuh", "attn_fwd.cuh", "attn_fwd_pp.cuh", "attn_bwd.cuh", "dequantize.cuh"]
+HEADERS = ["ptx.cuh", "quantize.cuh", "attn_fwd.cuh", "attn_fwd_pp.cuh", "attn_bwd.cuh", "dequantize.cuh",
+           "qk_norm_rope.cuh", "kv4.cuh", "attn_kv4.cuh"]
 
 
 def nvcc_path() -> str:

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -20,6 +21,9 @@
 #include "attn_bwd.cuh"
 #include "quantize.cuh"
 #include "dequantize.cuh"
+#include "qk_norm_rope.cuh"
+#include "kv4.cuh"
+#include "attn_kv4.cuh"
 
 namespace {
 
@@ -742,6 +746,412 @@ lpfa_status lpfa_attn_fwd_varlen_noalloc(const uint8_t* q, const uint8_t* q_sf, 
                        v_descale, out_bf16, lse, stream, 0, 0, true, scratch, static_cast<size_t>(LPFA_NOALLOC_SCRATCH_BYTES));
 }
 
+// ---------------------------------------------------------------------------------------
+// Norm and rotation of Q and K
+// ---------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxRopeHeads = 1024;
+
+bool rows_aligned(const lpfa_rows* r, lpfa_in_dtype dt) {
+  const int vec = dt == LPFA_IN_BF16 ? 8 : 4;
+  return aligned16(r->ptr) && r->tok_stride % vec == 0 && r->head_stride % vec == 0;
+}
+
+// An input (or output) of `name`, with `heads` heads where that is not 0.
+lpfa_status check_rows(const lpfa_rows* r, const char* name, lpfa_in_dtype dt, int heads) {
+  if (!r || !r->ptr) return fail(LPFA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (r->heads < 1) return fail(LPFA_ERR_INVALID_ARG, "%s has %d heads", name, r->heads);
+  if (heads && r->heads != heads)
+    return fail(LPFA_ERR_INVALID_ARG, "%s has %d heads, expected %d", name, r->heads, heads);
+  if (!rows_aligned(r, dt))
+    return fail(LPFA_ERR_INVALID_ARG, "%s must be 16-byte aligned with strides multiple of %d elements", name,
+                dt == LPFA_IN_BF16 ? 8 : 4);
+  return LPFA_OK;
+}
+
+// Validates what the three entry points share and fills the parameters and the plan. k may be absent.
+lpfa_status rope_setup(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int64_t tokens, int32_t head_dim,
+                       const lpfa_norm_rope* op, lpfa::RopeParams* p, lpfa::RopePlan* plan) {
+  if (dt != LPFA_IN_BF16 && dt != LPFA_IN_FP32) return fail(LPFA_ERR_INVALID_ARG, "invalid input dtype %d", dt);
+  if (head_dim != 128) return fail(LPFA_ERR_INVALID_ARG, "head_dim must be 128 (got %d)", head_dim);
+  if (tokens < 1 || tokens > INT32_MAX) return fail(LPFA_ERR_INVALID_ARG, "tokens must be in [1, 2^31)");
+  if (!op) return fail(LPFA_ERR_INVALID_ARG, "the norm and rotation (op) is NULL");
+  const bool has_k = k && k->heads != 0;
+  lpfa_status st;
+  if ((st = check_rows(q, "q", dt, 0)) != LPFA_OK) return st;
+  if (has_k && (st = check_rows(k, "k", dt, 0)) != LPFA_OK) return st;
+  if (static_cast<int64_t>(q->heads) + (has_k ? k->heads : 0) > kMaxRopeHeads)
+    return fail(LPFA_ERR_INVALID_ARG, "more than %d heads", kMaxRopeHeads);
+  if (op->norm != 0 && op->norm != 1) return fail(LPFA_ERR_INVALID_ARG, "norm must be 0 or 1");
+  if (op->norm && !(op->eps >= 0.f && std::isfinite(op->eps)))
+    return fail(LPFA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (op->q_weight || op->k_weight) {
+    if (op->weight_dtype != LPFA_IN_BF16 && op->weight_dtype != LPFA_IN_FP32)
+      return fail(LPFA_ERR_INVALID_ARG, "invalid weight dtype %d", op->weight_dtype);
+    const int vec = op->weight_dtype == LPFA_IN_BF16 ? 8 : 4;
+    if (!aligned16(op->q_weight) || !aligned16(op->k_weight) || op->q_weight_head_stride % vec ||
+        op->k_weight_head_stride % vec)
+      return fail(LPFA_ERR_INVALID_ARG, "weights must be 16-byte aligned with strides multiple of %d elements", vec);
+  }
+  *p = lpfa::RopeParams{};
+  *plan = lpfa::RopePlan{};
+  if (op->rotary) {
+    const lpfa_rotary* r = op->rotary;
+    if (r->axes < 1 || r->axes > 8) return fail(LPFA_ERR_INVALID_ARG, "a rotation has 1 to 8 axes (got %d)", r->axes);
+    if (r->pairing != LPFA_PAIR_INTERLEAVED && r->pairing != LPFA_PAIR_HALF)
+      return fail(LPFA_ERR_INVALID_ARG, "invalid pairing %d", r->pairing);
+    if (!op->positions) return fail(LPFA_ERR_INVALID_ARG, "positions is NULL");
+    if (reinterpret_cast<uintptr_t>(op->positions) % (op->pos_int64 ? 8 : 4))
+      return fail(LPFA_ERR_INVALID_ARG, "positions are not aligned to their type");
+    for (int i = 0; i < 64; ++i) {
+      if (!std::isfinite(r->inv_freq[i])) return fail(LPFA_ERR_INVALID_ARG, "frequency %d is not finite", i);
+      if (r->axis[i] >= r->axes) return fail(LPFA_ERR_INVALID_ARG, "pair %d is on axis %d of %d", i, r->axis[i], r->axes);
+      plan->turns[i] = r->inv_freq[i] / 6.283185307179586476925;
+      plan->axis[i] = r->axis[i];
+    }
+    p->pos = op->positions;
+    p->pos_tok = op->pos_tok_stride;
+    p->pos_axis = op->pos_axis_stride;
+    p->pos64 = op->pos_int64 ? 1 : 0;
+  }
+  p->tokens = tokens;
+  p->norm = op->norm;
+  p->eps = op->eps;
+  p->w_bf16 = op->weight_dtype == LPFA_IN_BF16 ? 1 : 0;
+  const lpfa_rows* in[2] = {q, has_k ? k : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    lpfa::RopeTensor& t = p->t[i];
+    t.x = in[i]->ptr;
+    t.tok_stride = in[i]->tok_stride;
+    t.head_stride = in[i]->head_stride;
+    t.heads = in[i]->heads;
+    t.w = i ? op->k_weight : op->q_weight;
+    t.w_head = t.w && t.heads > 1 ? (i ? op->k_weight_head_stride : op->q_weight_head_stride) : 0;
+  }
+  return LPFA_OK;
+}
+
+int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
+  return !w || heads < 1 ? 0 : (head_stride != 0 ? heads : 1);
+}
+
+}  // namespace
+
+extern "C++" {
+template <int kOut>
+static lpfa_status launch_rope(bool fp32, bool half, unsigned grid, size_t smem, const lpfa::RopeParams& p,
+                               const lpfa::RopePlan& plan, void* stream) {
+  auto kernel = fp32 ? (half ? lpfa::qk_norm_rope_kernel<float, kOut, true> : lpfa::qk_norm_rope_kernel<float, kOut, false>)
+                     : (half ? lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, true>
+                             : lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, false>);
+  kernel<<<grid, lpfa::kRopeThreads, smem, static_cast<cudaStream_t>(stream)>>>(p, plan);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation launch");
+}
+}  // extern "C++"
+
+lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int64_t tokens,
+                              int32_t head_dim, const lpfa_norm_rope* op, const lpfa_rows* q_out,
+                              const lpfa_rows* k_out, lpfa_in_dtype out_dt, void* stream) {
+  lpfa::RopeParams p;
+  lpfa::RopePlan plan;
+  lpfa_status st = rope_setup(q, k, dt, tokens, head_dim, op, &p, &plan);
+  if (st != LPFA_OK) return st;
+  if (out_dt != LPFA_IN_BF16 && out_dt != LPFA_IN_FP32) return fail(LPFA_ERR_INVALID_ARG, "invalid output dtype %d", out_dt);
+  const lpfa_rows* out[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i) {
+    if (!p.t[i].heads) continue;
+    if ((st = check_rows(out[i], i ? "k_out" : "q_out", out_dt, p.t[i].heads)) != LPFA_OK) return st;
+    if (out[i]->ptr == p.t[i].x && (out_dt != dt || (tokens > 1 && out[i]->tok_stride != p.t[i].tok_stride) ||
+                                    (p.t[i].heads > 1 && out[i]->head_stride != p.t[i].head_stride)))
+      return fail(LPFA_ERR_INVALID_ARG, "an output in its input's place needs its dtype and strides");
+    p.t[i].out = out[i]->ptr;
+    p.t[i].out_tok = out[i]->tok_stride;
+    p.t[i].out_head = out[i]->head_stride;
+  }
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  // Few tokens: one per block, so that the launch fills the card; else the angles of up to eight
+  // tokens are computed by as many threads as there are.
+  p.tile = static_cast<int>(std::min<int64_t>(lpfa::kRopeTile, (tokens + 4 * info.sms - 1) / (4 * info.sms)));
+  const unsigned grid = static_cast<unsigned>((tokens + p.tile - 1) / p.tile);
+  const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
+  return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream)
+                                : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream);
+}
+
+lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int32_t head_dim,
+                                    const lpfa_varlen_meta* meta, const lpfa_norm_rope* op, lpfa_scaling_mode mode,
+                                    uint8_t* q_payload, uint8_t* q_scales, uint8_t* k_payload, uint8_t* k_scales,
+                                    void* stream) {
+  lpfa_status st = check_meta(meta, "meta");
+  if (st != LPFA_OK) return st;
+  lpfa::RopeParams p;
+  lpfa::RopePlan plan;
+  if ((st = rope_setup(q, k, dt, meta->total_tokens, head_dim, op, &p, &plan)) != LPFA_OK) return st;
+  if (mode != LPFA_SCALE_RCEIL && mode != LPFA_SCALE_FLOOR) return fail(LPFA_ERR_INVALID_ARG, "invalid scaling mode %d", mode);
+  uint8_t* payload[2] = {q_payload, k_payload};
+  uint8_t* scales[2] = {q_scales, k_scales};
+  for (int i = 0; i < 2; ++i) {
+    if (!p.t[i].heads) continue;
+    if (!payload[i] || !scales[i]) return fail(LPFA_ERR_INVALID_ARG, "NULL payload or scales");
+    if (!aligned16(payload[i]) || !aligned16(scales[i]))
+      return fail(LPFA_ERR_INVALID_ARG, "payload and scales must be 16-byte aligned");
+    p.t[i].out = payload[i];
+    p.t[i].scales = scales[i];
+  }
+  p.num_seqs = meta->num_seqs;
+  p.cu_seqlens = meta->dev;
+  p.scale_off = meta->dev + meta->num_seqs + 1;
+  p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
+  if (meta->total_scale_blocks > INT32_MAX / 16) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
+  const size_t smem = static_cast<size_t>(p.t[0].heads + p.t[1].heads) * lpfa::kRopeTile * 4;
+  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half, static_cast<unsigned>(meta->total_scale_blocks) * 16u,
+                                       smem, p, plan, stream);
+}
+
+size_t lpfa_qk_norm_rope_bwd_workspace_bytes(int32_t q_heads, int32_t k_heads, const lpfa_norm_rope* op) {
+  if (!op || q_heads < 1 || k_heads < 0) return 0;
+  return static_cast<size_t>(rope_weight_rows(op->q_weight, op->q_weight_head_stride, q_heads) +
+                             rope_weight_rows(op->k_weight, op->k_weight_head_stride, k_heads)) *
+         128u * sizeof(float) * lpfa::kRopeBwdBlocks;
+}
+
+lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_out, const lpfa_rows* q,
+                                  const lpfa_rows* k, lpfa_in_dtype dt, int64_t tokens, int32_t head_dim,
+                                  const lpfa_norm_rope* op, const lpfa_rows* dq, const lpfa_rows* dk,
+                                  float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  lpfa::RopeParams p;
+  lpfa::RopePlan plan;
+  lpfa_status st = rope_setup(q, k, dt, tokens, head_dim, op, &p, &plan);
+  if (st != LPFA_OK) return st;
+  const lpfa_rows* in[2] = {dq_out, dk_out};
+  const lpfa_rows* out[2] = {dq, dk};
+  float* dw[2] = {dq_weight, dk_weight};
+  for (int i = 0; i < 2; ++i) {
+    lpfa::RopeTensor& t = p.t[i];
+    if (!t.heads) continue;
+    if ((st = check_rows(in[i], i ? "dk_out" : "dq_out", dt, t.heads)) != LPFA_OK) return st;
+    if ((st = check_rows(out[i], i ? "dk" : "dq", dt, t.heads)) != LPFA_OK) return st;
+    if (out[i]->ptr == in[i]->ptr && ((tokens > 1 && out[i]->tok_stride != in[i]->tok_stride) ||
+                                      (t.heads > 1 && out[i]->head_stride != in[i]->head_stride)))
+      return fail(LPFA_ERR_INVALID_ARG, "an output in its input's place needs its strides");
+    t.dy = in[i]->ptr;
+    t.dy_tok = in[i]->tok_stride;
+    t.dy_head = in[i]->head_stride;
+    t.out = out[i]->ptr;
+    t.out_tok = out[i]->tok_stride;
+    t.out_head = out[i]->head_stride;
+    p.w_rows[i] = rope_weight_rows(t.w, i ? op->k_weight_head_stride : op->q_weight_head_stride, t.heads);
+    if (p.w_rows[i] && (!dw[i] || !aligned16(dw[i])))
+      return fail(LPFA_ERR_INVALID_ARG, "%s must be a 16-byte aligned buffer", i ? "dk_weight" : "dq_weight");
+  }
+  const int rows = p.w_rows[0] + p.w_rows[1];
+  const size_t need = static_cast<size_t>(rows) * 128u * sizeof(float) * lpfa::kRopeBwdBlocks;
+  if (need) {
+    if (!workspace || !aligned16(workspace))
+      return fail(LPFA_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
+    if (workspace_bytes < need)
+      return fail(LPFA_ERR_INVALID_ARG, "workspace of %zu bytes is too small (%zu needed)", workspace_bytes, need);
+  }
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  p.partials = static_cast<float*>(workspace);
+  p.tile = static_cast<int>((tokens + lpfa::kRopeBwdBlocks - 1) / lpfa::kRopeBwdBlocks);
+  const int blocks = static_cast<int>((tokens + p.tile - 1) / p.tile);
+  const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
+  auto kernel = dt == LPFA_IN_FP32
+                    ? (half ? lpfa::qk_norm_rope_bwd_kernel<float, true> : lpfa::qk_norm_rope_bwd_kernel<float, false>)
+                    : (half ? lpfa::qk_norm_rope_bwd_kernel<__nv_bfloat16, true>
+                            : lpfa::qk_norm_rope_bwd_kernel<__nv_bfloat16, false>);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  kernel<<<blocks, lpfa::kRopeThreads, 0, s>>>(p, plan);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation backward launch");
+  if (rows) {
+    lpfa::qk_norm_rope_dw_kernel<<<rows, 1024, 0, s>>>(p.partials, blocks, rows, p.w_rows[0], dq_weight, dk_weight);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+  }
+  return LPFA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// MXFP4 cache
+// ---------------------------------------------------------------------------------------
+namespace {
+
+lpfa_status kv4_setup(const lpfa_kv4_cache* c, const lpfa_page_table* table, int32_t head_dim, lpfa::Kv4Cache* out) {
+  if (!c || !c->k || !c->k_sf || !c->v || !c->v_sf) return fail(LPFA_ERR_INVALID_ARG, "the cache is NULL");
+  if (!table || !table->ptr) return fail(LPFA_ERR_INVALID_ARG, "the page table is NULL");
+  if (head_dim != 128) return fail(LPFA_ERR_INVALID_ARG, "head_dim must be 128 (got %d)", head_dim);
+  if (c->num_pages < 1 || c->heads < 1 || c->heads > kMaxRopeHeads)
+    return fail(LPFA_ERR_INVALID_ARG, "the cache has %d pages of %d heads", c->num_pages, c->heads);
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != c->page_size) ++shift;
+  if ((1 << shift) != c->page_size)
+    return fail(LPFA_ERR_INVALID_ARG, "page_size must be 16, 32, 64, 128 or 256 (got %d)", c->page_size);
+  if (!aligned16(c->k) || !aligned16(c->k_sf) || !aligned16(c->v) || !aligned16(c->v_sf))
+    return fail(LPFA_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+  if (table->width < 1 || (static_cast<int64_t>(table->width) << shift) > (int64_t{1} << 30))
+    return fail(LPFA_ERR_INVALID_ARG, "the page table must hold 1 to 2^30 tokens per sequence");
+  if (reinterpret_cast<uintptr_t>(table->ptr) % 4) return fail(LPFA_ERR_INVALID_ARG, "the page table is misaligned");
+  out->payload[0] = c->k;
+  out->payload[1] = c->v;
+  out->scales[0] = c->k_sf;
+  out->scales[1] = c->v_sf;
+  out->pages = c->num_pages;
+  out->heads = c->heads;
+  out->page_size = c->page_size;
+  out->page_shift = shift;
+  out->table = table->ptr;
+  out->table_stride = table->seq_stride;
+  out->width = table->width;
+  return LPFA_OK;
+}
+
+}  // namespace
+
+lpfa_status lpfa_kv4_write(const lpfa_rows* k, const lpfa_rows* v, lpfa_in_dtype dt, int32_t head_dim,
+                           const lpfa_kv4_cache* cache, const lpfa_page_table* table, const int32_t* start,
+                           const lpfa_varlen_meta* meta, lpfa_scaling_mode mode, void* stream) {
+  lpfa::Kv4WriteParams p = {};
+  lpfa_status st = kv4_setup(cache, table, head_dim, &p.c);
+  if (st != LPFA_OK) return st;
+  if (dt != LPFA_IN_BF16 && dt != LPFA_IN_FP32) return fail(LPFA_ERR_INVALID_ARG, "invalid input dtype %d", dt);
+  if (mode != LPFA_SCALE_RCEIL && mode != LPFA_SCALE_FLOOR) return fail(LPFA_ERR_INVALID_ARG, "invalid scaling mode %d", mode);
+  if ((st = check_meta(meta, "meta")) != LPFA_OK) return st;
+  const lpfa_rows* in[2] = {k, v};
+  for (int i = 0; i < 2; ++i) {
+    if ((st = check_rows(in[i], i ? "v" : "k", dt, cache->heads)) != LPFA_OK) return st;
+    p.x[i] = in[i]->ptr;
+    p.tok_stride[i] = in[i]->tok_stride;
+    p.head_stride[i] = in[i]->head_stride;
+  }
+  if (reinterpret_cast<uintptr_t>(start) % 4) return fail(LPFA_ERR_INVALID_ARG, "start is misaligned");
+  p.num_seqs = meta->num_seqs;
+  p.cu_seqlens = meta->dev;
+  p.start = start;
+  p.tokens = meta->total_tokens;
+  p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  // As for the rotation: a token per block while there are few.
+  p.tile = std::min(lpfa::kKv4Tile, (p.tokens + 4 * info.sms - 1) / (4 * info.sms));
+  const dim3 grid(static_cast<unsigned>((p.tokens + p.tile - 1) / p.tile), 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dt == LPFA_IN_FP32)
+    lpfa::kv4_write_kernel<float><<<grid, lpfa::kKv4Threads, 0, s>>>(p);
+  else
+    lpfa::kv4_write_kernel<__nv_bfloat16><<<grid, lpfa::kKv4Threads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache write launch");
+}
+
+lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* table, const int32_t* start,
+                          const lpfa_varlen_meta* meta, int32_t head_dim, uint8_t* k_payload, uint8_t* k_scales,
+                          uint8_t* v_payload, uint8_t* v_scales, void* stream) {
+  lpfa::Kv4ReadParams p = {};
+  lpfa_status st = kv4_setup(cache, table, head_dim, &p.c);
+  if (st != LPFA_OK) return st;
+  if ((st = check_meta(meta, "meta")) != LPFA_OK) return st;
+  if (!k_payload || !k_scales || !v_payload || !v_scales) return fail(LPFA_ERR_INVALID_ARG, "NULL payload or scales");
+  if (!aligned16(k_payload) || !aligned16(k_scales) || !aligned16(v_payload) || !aligned16(v_scales))
+    return fail(LPFA_ERR_INVALID_ARG, "payload and scales must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(start) % 4) return fail(LPFA_ERR_INVALID_ARG, "start is misaligned");
+  if (meta->total_scale_blocks > INT32_MAX / 16) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
+  p.payload[0] = k_payload;
+  p.payload[1] = v_payload;
+  p.scales[0] = k_scales;
+  p.scales[1] = v_scales;
+  p.num_seqs = meta->num_seqs;
+  p.cu_seqlens = meta->dev;
+  p.scale_off = meta->dev + meta->num_seqs + 1;
+  p.start = start;
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * 16u, 2);
+  lpfa::kv4_read_kernel<<<grid, lpfa::kKv4Threads, static_cast<size_t>(cache->heads) * 32,
+                          static_cast<cudaStream_t>(stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache read launch");
+}
+
+extern "C++" {
+template <int kTiles>
+static lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, cudaStream_t s) {
+  constexpr uint32_t smem = lpfa::attn4_smem_bytes<kTiles>();
+  auto kernel = lpfa::attn_kv4_kernel<kTiles>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  const int64_t tiles = (max_rows + 8 * kTiles - 1) / (8 * kTiles);
+  const int64_t work = tiles * p.c.heads * p.num_seqs;
+  if (work > INT32_MAX / lpfa::kAttn4MaxSplit) return fail(LPFA_ERR_INVALID_ARG, "too many query tiles");
+  p.tiles = static_cast<int>(tiles);
+  // Blocks for a few waves of three per SM (ragged lengths need the slack), but a split of at least
+  // 256 keys, two tiles for each of its warps.
+  const int64_t keys = static_cast<int64_t>(p.c.width) << p.c.page_shift;
+  p.splits = 1;
+  while (p.splits < lpfa::kAttn4MaxSplit && work * p.splits < 6 * sms && keys >= 2 * 256 * static_cast<int64_t>(p.splits))
+    p.splits *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(work * p.splits));
+  cfg.blockDim = dim3(lpfa::kAttn4Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache attention launch");
+}
+}  // extern "C++"
+
+lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_kv4_cache* cache,
+                              const lpfa_page_table* table, const int32_t* kv_lens, const lpfa_varlen_meta* meta_q,
+                              int32_t causal, void* out_bf16, float* lse, void* stream) {
+  lpfa::Attn4Params p = {};
+  lpfa_status st = kv4_setup(cache, table, head_dim, &p.c);
+  if (st != LPFA_OK) return st;
+  if ((st = check_rows(q, "q", LPFA_IN_BF16, 0)) != LPFA_OK) return st;
+  if ((st = check_meta(meta_q, "meta_q")) != LPFA_OK) return st;
+  if (!kv_lens || !out_bf16 || !lse) return fail(LPFA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (q->heads % cache->heads || q->heads > 65536)
+    return fail(LPFA_ERR_INVALID_ARG, "%d query heads over %d cached heads: not a multiple", q->heads, cache->heads);
+  if (causal != 0 && causal != 1) return fail(LPFA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!aligned16(out_bf16) || !aligned16(lse) || reinterpret_cast<uintptr_t>(kv_lens) % 4)
+    return fail(LPFA_ERR_INVALID_ARG, "out and lse must be 16-byte aligned, kv_lens 4-byte aligned");
+  p.q = static_cast<const __nv_bfloat16*>(q->ptr);
+  p.q_tok = q->tok_stride;
+  p.q_head = q->head_stride;
+  p.cu_q = meta_q->dev;
+  p.kv_lens = kv_lens;
+  p.num_seqs = meta_q->num_seqs;
+  p.heads_q = q->heads;
+  p.group = q->heads / cache->heads;
+  p.causal = causal;
+  p.total_q = meta_q->total_tokens;
+  p.out = static_cast<__nv_bfloat16*>(out_bf16);
+  p.lse = lse;
+  const int64_t max_rows = static_cast<int64_t>(meta_q->max_seqlen) * p.group;
+  if (max_rows > INT32_MAX / 2) return fail(LPFA_ERR_INVALID_ARG, "too many query rows in a sequence");
+  DeviceInfo info;
+  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // One row costs what eight do: eight rows per block where that is all there are, else sixteen, which
+  // halves the reads of the cache.
+  return max_rows <= 8 ? launch_attn_kv4<1>(p, max_rows, info.sms, s) : launch_attn_kv4<2>(p, max_rows, info.sms, s);
+}
+
 lpfa_status lpfa_device_status(void* stream, int32_t* detail) {
   if (detail) *detail = 0;
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
@@ -754,6 +1164,9 @@ lpfa_status lpfa_device_status(void* stream, int32_t* detail) {
     e = cudaMemcpyToSymbol(lpfa::g_lpfa_status, zero, sizeof(zero));
     if (e != cudaSuccess) return cuda_fail(e, "resetting the device status word");
     if (detail) *detail = word[1];
+    if (word[0] == LPFA_ERR_INVALID_ARG)
+      return fail(LPFA_ERR_INVALID_ARG, "a length, start or page table entry in device memory is out of range (site %d)",
+                  word[1]);
     return fail(LPFA_ERR_TIMEOUT, "a kernel gave up waiting on a barrier (site %d)", word[1]);
   }
   return LPFA_OK;
