@@ -516,28 +516,25 @@ class _Scope:
     work runs on (its allocator pool), so neither earlier nor later work of another stream can share
     their memory; `seen_by_caller` marks results that the caller's own stream will go on to read."""
 
+    __slots__ = ("device", "handle", "restore", "other", "caller")
+
     def __init__(self, device, stream):
         self.device = device
-        self.restore = None
-        index = device.index
-        if index is not None and index != torch.cuda.current_device():
-            self.restore = torch.cuda.device(device)
-        self.other = None
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.other = stream
-        self.stream = stream
+        self.restore = None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+        self.other = stream
 
     def __enter__(self):
         if self.restore is not None:
             self.restore.__enter__()
-        self.caller = torch.cuda.current_stream()
-        if self.other is None or self.other.cuda_stream == self.caller.cuda_stream:
+        self.handle = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if self.other is not None:
+            stream = self.other
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
             self.other = None
-            self.handle = self.caller.cuda_stream
-        else:
-            self.handle = self.other.cuda_stream
+            if stream.cuda_stream != self.handle:
+                self.caller = torch.cuda.current_stream()
+                self.handle, self.other = stream.cuda_stream, stream
         return self
 
     def __exit__(self, *exc):
@@ -553,30 +550,37 @@ class _Scope:
             t.record_stream(self.caller)
         return t
 
+    def like(self, x, dtype):
+        """A new contiguous tensor of x's shape."""
+        if self.other is None:
+            return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+        return self.empty(x.shape, dtype)
 
-def _rows(t: Optional[torch.Tensor], name: str, dtype=None, device=None, shape=None) -> Optional[_Rows]:
-    """A (tokens, heads, 128) tensor as an lpfa_rows; None stays None."""
-    if t is None:
-        return None
-    if t.dim() != 3 or t.shape[2] != 128 or t.stride(2) != 1 or t.shape[0] < 1 or t.shape[1] < 1:
-        raise ValueError("%s must be a (tokens, heads, 128) tensor with a contiguous last dimension" % name)
-    if not t.is_cuda or (device is not None and t.device != device):
+
+def _rows(t: torch.Tensor, name: str, dtype, device, shape=None) -> _Rows:
+    """A (tokens, heads, 128) tensor as an lpfa_rows."""
+    s = t.shape
+    if len(s) != 3 or s[2] != 128 or 0 in s:
+        raise ValueError("%s must be a (tokens, heads, 128) tensor" % name)
+    if t.dtype != dtype or dtype not in _DTYPE_CODE:
+        raise ValueError("%s must be %s" % (name, dtype if dtype in _DTYPE_CODE else "bf16 or fp32"))
+    if not t.is_cuda or t.device != device:
         raise ValueError("%s must be on the CUDA device of the other tensors" % name)
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s" % (name, dtype))
-    if t.dtype not in _DTYPE_CODE:
-        raise ValueError("%s must be bf16 or fp32" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and s != shape:
         raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
     # The stride of an axis of one element is never stepped over; it may be anything.
-    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * 128,
-                 t.stride(1) if t.shape[1] > 1 else 128, t.shape[1])
+    return _Rows(t.data_ptr(), a if s[0] > 1 else s[1] * 128, b if s[1] > 1 else 128, s[1])
 
 
 def _out_rows(t: torch.Tensor, name: str, dtype, device, shape) -> _Rows:
     """As _rows, for a tensor that is written: its elements must be different memory."""
     r = _rows(t, name, dtype, device, shape)
-    lo, hi = sorted(((r.tok_stride, t.shape[0]), (r.head_stride, t.shape[1])))
+    if t.is_contiguous():
+        return r
+    lo, hi = sorted(((r.tok_stride, shape[0]), (r.head_stride, shape[1])))
     if (lo[0] < 128 and lo[1] > 1) or (hi[1] > 1 and hi[0] < (lo[0] * (lo[1] - 1) + 128 if lo[1] > 1 else 128)):
         raise ValueError("%s has rows that overlap" % name)
     return r
@@ -640,48 +644,61 @@ class RotaryAxes:
         self.axes, self.pairing = axes, pairing
         self.inv_freq, self.axis = tuple(freq), tuple(axis)
         self._c = _Rotary(axes, PAIRINGS[pairing], (ctypes.c_double * 64)(*freq), (ctypes.c_uint8 * 64)(*axis))
+        self._ptr = ctypes.pointer(self._c)
 
 
-def _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm) -> _NormRope:
-    op = _NormRope()
-    op.norm = 1 if norm else 0
-    op.eps = eps
+def _weight(w: torch.Tensor, name: str, heads: int, dtype, device):
+    """(address, stride between heads) of a weight."""
+    s = w.shape
+    if (s != (128,) and s != (heads, 128)) or not w.is_contiguous() or w.device != device:
+        raise ValueError("%s must be a contiguous (128,) or (heads, 128) tensor on the device of q" % name)
+    if w.dtype != dtype or dtype not in _DTYPE_CODE:
+        raise ValueError("weights must be bf16 or fp32, both the same")
+    return w.data_ptr(), 128 if len(s) == 2 else 0
+
+
+def _norm_rope_op(tokens, device, q_heads, k_heads, positions, rope, q_weight, k_weight, eps, norm) -> _NormRope:
     if norm and not (0.0 <= eps < float("inf")):
         raise ValueError("eps must be finite and >= 0")
+    rotary, pos, pt, pa, p64 = None, None, 0, 0, 0
     if rope is not None:
         if not isinstance(rope, RotaryAxes):
             raise ValueError("rope must be a RotaryAxes or None")
         if positions is None:
             raise ValueError("a rotation needs positions")
-        pos = positions.unsqueeze(1) if positions.dim() == 1 else positions
-        if pos.dim() != 2 or pos.shape[0] != q.shape[0] or pos.shape[1] < rope.axes:
-            raise ValueError("positions must be (tokens, axes): %d tokens, %d axes" % (q.shape[0], rope.axes))
-        if pos.dtype not in (torch.int32, torch.int64):
+        s = positions.shape
+        if not 1 <= len(s) <= 2 or s[0] != tokens or (s[1] if len(s) == 2 else 1) < rope.axes:
+            raise ValueError("positions must be (tokens, axes): %d tokens, %d axes" % (tokens, rope.axes))
+        if positions.dtype == torch.int64:
+            p64 = 1
+        elif positions.dtype != torch.int32:
             raise ValueError("positions must be int32 or int64")
-        if pos.device != q.device:
+        if positions.device != device:
             raise ValueError("positions must be on the device of q")
-        op.rotary = ctypes.pointer(rope._c)
-        op.positions = pos.data_ptr()
-        op.pos_tok_stride, op.pos_axis_stride = pos.stride(0), pos.stride(1)
-        op.pos_int64 = 1 if pos.dtype == torch.int64 else 0
-    wdt = None
-    for name, x, w in (("q", q, q_weight), ("k", k, k_weight)):
-        if w is None:
-            continue
-        if x is None:
+        rotary, pos, pt = rope._ptr, positions.data_ptr(), positions.stride(0)
+        if len(s) == 2:
+            pa = positions.stride(1)
+    qw, qs, kw, ks = None, 0, None, 0
+    first = q_weight if q_weight is not None else k_weight
+    if q_weight is not None:
+        qw, qs = _weight(q_weight, "q_weight", q_heads, first.dtype, device)
+    if k_weight is not None:
+        if not k_heads:
             raise ValueError("k_weight without k")
-        if w.dtype not in _DTYPE_CODE or (wdt is not None and w.dtype != wdt):
-            raise ValueError("weights must be bf16 or fp32, both the same")
-        if tuple(w.shape) not in ((128,), (x.shape[1], 128)) or not w.is_contiguous() or w.device != q.device:
-            raise ValueError("%s_weight must be a contiguous (128,) or (heads, 128) tensor on the device of q" % name)
-        wdt = w.dtype
-        stride = 128 if w.dim() == 2 else 0
-        if name == "q":
-            op.q_weight, op.q_weight_head_stride = w.data_ptr(), stride
-        else:
-            op.k_weight, op.k_weight_head_stride = w.data_ptr(), stride
-    op.weight_dtype = _DTYPE_CODE[wdt] if wdt is not None else 0
-    return op
+        kw, ks = _weight(k_weight, "k_weight", k_heads, first.dtype, device)
+    return _NormRope(rotary, pos, pt, pa, p64, 1 if norm else 0, eps, qw, qs, kw, ks,
+                     0 if first is None else _DTYPE_CODE[first.dtype])
+
+
+def _qk_rows(q, k):
+    """lpfa_rows of q and (None without it) k, and the number of k's heads."""
+    qr = _rows(q, "q", q.dtype, q.device)
+    if k is None:
+        return qr, None, 0
+    kr = _rows(k, "k", q.dtype, q.device)
+    if k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must have the same tokens")
+    return qr, kr, kr.heads
 
 
 def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -697,27 +714,28 @@ def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Opt
     (heads, 128), bf16 or fp32. norm=False leaves the norm out (the weight still applies).
     Outputs: out_dtype (the input's by default), contiguous unless given; an output may be its own input.
     """
-    qr = _rows(q, "q")
-    device, dt = q.device, q.dtype
-    kr = _rows(k, "k", dt, device)
-    if k is not None and k.shape[0] != q.shape[0]:
-        raise ValueError("q and k must have the same tokens")
+    qr, kr, k_heads = _qk_rows(q, k)
+    device, dt, shape = q.device, q.dtype, q.shape
     odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE_CODE:
         raise ValueError("out_dtype must be bf16 or fp32")
-    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    op = _norm_rope_op(shape[0], device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
+    ko = None
     with _Scope(device, stream) as sc:
         if q_out is None:
-            q_out = sc.empty(q.shape, odt)
-        qo = _out_rows(q_out, "q_out", odt, device, q.shape)
-        ko = None
-        if k is not None:
-            if k_out is None:
-                k_out = sc.empty(k.shape, odt)
+            q_out = sc.like(q, odt)
+            qo = _Rows(q_out.data_ptr(), shape[1] * 128, 128, shape[1])
+        else:
+            qo = _out_rows(q_out, "q_out", odt, device, shape)
+        if k is None:
+            if k_out is not None:
+                raise ValueError("k_out without k")
+        elif k_out is None:
+            k_out = sc.like(k, odt)
+            ko = _Rows(k_out.data_ptr(), k_heads * 128, 128, k_heads)
+        else:
             ko = _out_rows(k_out, "k_out", odt, device, k.shape)
-        elif k_out is not None:
-            raise ValueError("k_out without k")
-        _check(_lib.lpfa_qk_norm_rope(qr, kr, _DTYPE_CODE[dt], q.shape[0], 128, op, qo, ko, _DTYPE_CODE[odt], sc.handle))
+        _check(_lib.lpfa_qk_norm_rope(qr, kr, _DTYPE_CODE[dt], shape[0], 128, op, qo, ko, _DTYPE_CODE[odt], sc.handle))
     return q_out, k_out
 
 
@@ -730,34 +748,39 @@ def lpfa_qk_norm_rope_mxfp8(q: torch.Tensor, k: Optional[torch.Tensor], position
     """lpfa_qk_norm_rope straight into the attention's input: returns (q_payload, q_scales, k_payload,
     k_scales) as lpfa_quantize_mxfp8_varlen lays them out (None for k without k). The bytes are those
     of lpfa_qk_norm_rope with fp32 outputs and the quantizer after it."""
-    qr = _rows(q, "q")
-    device, dt = q.device, q.dtype
-    kr = _rows(k, "k", dt, device)
-    if k is not None and k.shape[0] != q.shape[0]:
-        raise ValueError("q and k must have the same tokens")
-    if q.shape[0] != meta.total_tokens:
-        raise ValueError("q has %d tokens but the metadata describes %d" % (q.shape[0], meta.total_tokens))
+    qr, kr, k_heads = _qk_rows(q, k)
+    device, dt, T = q.device, q.dtype, q.shape[0]
+    if T != meta.total_tokens:
+        raise ValueError("q has %d tokens but the metadata describes %d" % (T, meta.total_tokens))
     if scaling_mode not in SCALING_MODES:
         raise ValueError("scaling_mode must be 'rceil' or 'floor'")
+    if k is None and (k_payload is not None or k_scales is not None):
+        raise ValueError("k_payload or k_scales without k")
     _check_meta_device(meta, device)
-    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    op = _norm_rope_op(T, device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
     with _Scope(device, stream) as sc:
-        outs = []
-        for x, payload, scales, name in ((q, q_payload, q_scales, "q"), (k, k_payload, k_scales, "k")):
-            if x is None:
-                if payload is not None or scales is not None:
-                    raise ValueError("k_payload or k_scales without k")
-                outs += [None, None]
-                continue
-            T, H = x.shape[0], x.shape[1]
-            nb = (meta.scale_bytes(H),)
-            outs.append(sc.empty((T, H, 128), torch.uint8) if payload is None else
-                        _contiguous(payload, name + "_payload", torch.uint8, device, (T, H, 128)))
-            outs.append(sc.empty(nb, torch.uint8) if scales is None else
-                        _contiguous(scales, name + "_scales", torch.uint8, device, nb))
+        q_payload, q_scales = _mxfp8_out(sc, q, meta, q_payload, q_scales, "q")
+        kp = ks = None
+        if k is not None:
+            k_payload, k_scales = _mxfp8_out(sc, k, meta, k_payload, k_scales, "k")
+            kp, ks = k_payload.data_ptr(), k_scales.data_ptr()
         _check(_lib.lpfa_qk_norm_rope_mxfp8(qr, kr, _DTYPE_CODE[dt], 128, meta._c, op, SCALING_MODES[scaling_mode],
-                                            *[_ptr(x) for x in outs], sc.handle))
-    return tuple(outs)
+                                            q_payload.data_ptr(), q_scales.data_ptr(), kp, ks, sc.handle))
+    return q_payload, q_scales, k_payload, k_scales
+
+
+def _mxfp8_out(sc, x, meta, payload, scales, name):
+    """Payload and scale storage for x, new or checked."""
+    nb = meta.total_scale_blocks * x.shape[1] * 512
+    if payload is None:
+        payload = sc.like(x, torch.uint8)
+    else:
+        _contiguous(payload, name + "_payload", torch.uint8, x.device, x.shape)
+    if scales is None:
+        scales = sc.empty(nb, torch.uint8)
+    else:
+        _contiguous(scales, name + "_scales", torch.uint8, x.device, (nb,))
+    return payload, scales
 
 
 def lpfa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
@@ -772,22 +795,19 @@ def lpfa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
     for bf16); q, k and the rest as in the forward call. Weight gradients are fp32 in the weight's
     shape. dq may be dq_out's memory, dk dk_out's. Equal calls give equal bits.
     """
-    qr = _rows(q, "q")
-    device, dt = q.device, q.dtype
-    kr = _rows(k, "k", dt, device)
+    qr, kr, k_heads = _qk_rows(q, k)
+    device, dt, shape = q.device, q.dtype, q.shape
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out come together")
-    if k is not None and k.shape[0] != q.shape[0]:
-        raise ValueError("q and k must have the same tokens")
-    gq = _rows(dq_out, "dq_out", dt, device, q.shape)
+    gq = _rows(dq_out, "dq_out", dt, device, shape)
     gk = _rows(dk_out, "dk_out", dt, device, k.shape) if k is not None else None
-    op = _norm_rope_op(q, k, positions, rope, q_weight, k_weight, eps, norm)
+    op = _norm_rope_op(shape[0], device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
     with _Scope(device, stream) as sc:
-        dq = sc.empty(q.shape, dt) if dq is None else dq
-        dqr = _out_rows(dq, "dq", dt, device, q.shape)
+        dq = sc.like(q, dt) if dq is None else dq
+        dqr = _out_rows(dq, "dq", dt, device, shape)
         dkr = None
         if k is not None:
-            dk = sc.empty(k.shape, dt) if dk is None else dk
+            dk = sc.like(k, dt) if dk is None else dk
             dkr = _out_rows(dk, "dk", dt, device, k.shape)
         elif dk is not None:
             raise ValueError("dk without k")
@@ -798,11 +818,11 @@ def lpfa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
                     raise ValueError("%s without its weight" % name)
                 dws.append(None)
             else:
-                dws.append(sc.empty(w.shape, torch.float32) if dw is None else
+                dws.append(sc.like(w, torch.float32) if dw is None else
                            _contiguous(dw, name, torch.float32, device, w.shape))
-        need = _lib.lpfa_qk_norm_rope_bwd_workspace_bytes(q.shape[1], 0 if k is None else k.shape[1], op)
-        ws = sc.empty((need,), torch.uint8, seen_by_caller=False) if need else None
-        _check(_lib.lpfa_qk_norm_rope_bwd(gq, gk, qr, kr, _DTYPE_CODE[dt], q.shape[0], 128, op, dqr, dkr, _ptr(dws[0]),
+        need = _lib.lpfa_qk_norm_rope_bwd_workspace_bytes(shape[1], k_heads, op)
+        ws = sc.empty(need, torch.uint8, seen_by_caller=False) if need else None
+        _check(_lib.lpfa_qk_norm_rope_bwd(gq, gk, qr, kr, _DTYPE_CODE[dt], shape[0], 128, op, dqr, dkr, _ptr(dws[0]),
                                           _ptr(dws[1]), _ptr(ws), need, sc.handle))
     return dq, dk, dws[0], dws[1]
 
@@ -846,20 +866,20 @@ class Kv4Cache:
         self._c = _Kv4Cache(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), *k.shape[:3])
 
 
-def _page_table(page_table: torch.Tensor, num_seqs: int, device) -> _PageTable:
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != num_seqs or
-            page_table.shape[1] < 1 or (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
+def _page_table(t: torch.Tensor, num_seqs: int, device) -> _PageTable:
+    s = t.shape
+    if t.dtype != torch.int32 or len(s) != 2 or s[0] != num_seqs or s[1] < 1 or (s[1] > 1 and t.stride(1) != 1):
         raise ValueError("page_table must be an int32 (sequences, pages) tensor with contiguous rows: %d sequences"
                          % num_seqs)
-    if page_table.device != device:
+    if t.device != device:
         raise ValueError("page_table must be on the device of the cache")
-    return _PageTable(page_table.data_ptr(), page_table.stride(0), page_table.shape[1])
+    return _PageTable(t.data_ptr(), t.stride(0), s[1])
 
 
 def _seq_ints(t: Optional[torch.Tensor], name: str, num_seqs: int, device) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != (num_seqs,) or not t.is_contiguous() or t.device != device:
+    if t.dtype != torch.int32 or t.shape != (num_seqs,) or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous int32 tensor of %d sequences on the device of the cache" % (name, num_seqs))
     return t.data_ptr()
 
@@ -874,7 +894,7 @@ def lpfa_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, page_table
     and reported by lpfa_device_status. Two tokens of a call must not share a slot.
     """
     device = cache.device
-    kr = _rows(k, "k", None, device)
+    kr = _rows(k, "k", k.dtype, device)
     vr = _rows(v, "v", k.dtype, device, k.shape)
     if k.shape[1] != cache.heads:
         raise ValueError("k has %d heads, the cache %d" % (k.shape[1], cache.heads))
@@ -901,14 +921,16 @@ def lpfa_kv4_read(cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta, s
     table = _page_table(page_table, meta.num_seqs, device)
     starts = _seq_ints(start, "start", meta.num_seqs, device)
     T, H = meta.total_tokens, cache.heads
-    nb = meta.scale_bytes(H)
+    nb = meta.total_scale_blocks * H * 512
     with _Scope(device, stream) as sc:
         outs = []
         for t, name, shape in ((k_payload, "k_payload", (T, H, 128)), (k_scales, "k_scales", (nb,)),
                                (v_payload, "v_payload", (T, H, 128)), (v_scales, "v_scales", (nb,))):
             outs.append(sc.empty(shape, torch.uint8) if t is None else _contiguous(t, name, torch.uint8, device, shape))
-        _check(_lib.lpfa_kv4_read(cache._c, table, starts, meta._c, 128, *[t.data_ptr() for t in outs], sc.handle))
-    return tuple(outs)
+        k, ks, v, vs = outs
+        _check(_lib.lpfa_kv4_read(cache._c, table, starts, meta._c, 128, k.data_ptr(), ks.data_ptr(), v.data_ptr(),
+                                  vs.data_ptr(), sc.handle))
+    return k, ks, v, vs
 
 
 def lpfa_attn_fwd_kv4(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -935,8 +957,14 @@ def lpfa_attn_fwd_kv4(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor
         raise ValueError("kv_lens is needed")
     lens = _seq_ints(kv_lens, "kv_lens", meta_q.num_seqs, device)
     with _Scope(device, stream) as sc:
-        out = sc.empty((Tq, H, 128), torch.bfloat16) if out is None else _contiguous(out, "out", torch.bfloat16, device, (Tq, H, 128))
-        lse = sc.empty((H, Tq), torch.float32) if lse is None else _contiguous(lse, "lse", torch.float32, device, (H, Tq))
+        if out is None:
+            out = sc.like(q, torch.bfloat16)
+        else:
+            _contiguous(out, "out", torch.bfloat16, device, q.shape)
+        if lse is None:
+            lse = sc.empty((H, Tq), torch.float32)
+        else:
+            _contiguous(lse, "lse", torch.float32, device, (H, Tq))
         _check(_lib.lpfa_attn_fwd_kv4(qr, 128, cache._c, table, lens, meta_q._c, 1 if causal else 0, out.data_ptr(),
                                       lse.data_ptr(), sc.handle))
     return out, lse

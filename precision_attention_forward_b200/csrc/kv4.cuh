@@ -15,10 +15,13 @@
 // E2M1 is a subset of E4M3 and the scale rule's power of two is the same kind of byte, so reading a
 // cached row back as MXFP8 is exact: codes are looked up, scales are copied.
 //
-// Both kernels stream; HBM bounds them. A row of 128 is 16 lanes: lane m holds bytes 4m..4m+3, i.e.
-// two runs of four elements in two scale blocks. Page entries are looked up once per token and
-// block of threads; one outside the table or the pool skips its token and records
-// LPFA_ERR_INVALID_ARG in the device status word.
+// Both kernels stream; HBM bounds them. Four lanes own a row: lane t holds the row's 16 bytes 16 t ..
+// 16 t + 15, which are the elements 8 t .. 8 t + 7 of each of the four scale blocks, so a lane reads
+// (or writes) whole 16-byte (8-byte) runs, a block's maximum is two shuffles, and a warp moves eight
+// rows at a time. (With 16 lanes to a row, four bytes each, the same work took 81 and 49 warp
+// instructions a row for writing and reading and reached a third of the copy bandwidth.) Page entries
+// are looked up once per token and block of threads; one outside the table or the pool skips its token
+// and records LPFA_ERR_INVALID_ARG in the device status word.
 #pragma once
 
 #include <cstdint>
@@ -31,8 +34,8 @@
 namespace lpfa {
 
 constexpr int kKv4Threads = 256;
-constexpr int kKv4Tile = 16;  // tokens of a writing block (at most)
-constexpr int kKv4Batch = 4;  // rows that a half warp has in flight
+constexpr int kKv4Tile = 32;  // tokens of a block, at most
+constexpr int kKv4Rows = kKv4Threads / 4;  // rows that a block has in hand at a time
 
 // Sites of the status word for entries out of range.
 enum Kv4Site : int { kKv4WriteSite = 300, kKv4ReadSite = 301, kKv4AttnLenSite = 302, kKv4AttnPageSite = 303 };
@@ -101,84 +104,76 @@ struct Kv4WriteParams {
   int floor_mode;
 };
 
-template <typename T>
-__device__ __forceinline__ void kv4_load4(const T* p, float (&v)[4]);
-template <>
-__device__ __forceinline__ void kv4_load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
-template <>
-__device__ __forceinline__ void kv4_load4<float>(const float* p, float (&v)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-
-// Grid (token tiles, 2): K for y = 0, V for y = 1. Rows are taken token by token within a head, so
-// that the 64-byte rows that neighbouring half warps write are neighbours in the page.
+// Grid (token tiles, 2): K for y = 0, V for y = 1. Rows are taken token by token within a head: the
+// 64-byte rows that neighbouring lanes write are neighbours in the page, and what they read are whole
+// 256-byte (512-byte) rows.
 template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   __shared__ int64_t slot_of[kKv4Tile];
-  const int lane = threadIdx.x & 31, l16 = lane & 15, hw = threadIdx.x >> 4;
+  const int t = threadIdx.x & 3;
   const int tok0 = blockIdx.x * p.tile;
   const int ntok = min(p.tile, p.tokens - tok0);
   const int y = blockIdx.y;
   if (threadIdx.x < ntok) {
     const int tok = tok0 + threadIdx.x;
     const int seq = find_seq(p.cu_seqlens, p.num_seqs, tok);
-    const int64_t at = static_cast<int64_t>(tok) - __ldg(p.cu_seqlens + seq) + (p.start ? __ldg(p.start + seq) : 0);
-    const bool ok = !p.start || __ldg(p.start + seq) >= 0;
-    slot_of[threadIdx.x] = kv4_slot(p.c, seq, ok ? at : -1, kKv4WriteSite);
+    const int start = p.start ? __ldg(p.start + seq) : 0;
+    const int64_t at = static_cast<int64_t>(tok) - __ldg(p.cu_seqlens + seq) + start;
+    slot_of[threadIdx.x] = kv4_slot(p.c, seq, start >= 0 ? at : -1, kKv4WriteSite);
   }
   __syncthreads();
-  const T* x = static_cast<const T*>(p.x[y]);
-  const int g = l16 >> 1;        // run of four elements within a block
-  const int b0 = (l16 & 1) * 2;  // this lane's two blocks: b0, b0 + 1
+  const T* x = static_cast<const T*>(p.x[y]) + tok0 * p.tok_stride[y] + 8 * t;
   const int rows = ntok * p.c.heads;
   const float per_tok = 1.f / static_cast<float>(ntok);
-  constexpr int kHalves = kKv4Threads / 16;
 #pragma unroll 1
-  for (int base = hw & ~1; base < rows; base += kHalves * kKv4Batch) {
-    float v[kKv4Batch][2][4];
-    int64_t row[kKv4Batch];
+  for (int base = (threadIdx.x >> 5) * 8; base < rows; base += kKv4Rows) {  // the same for the whole warp
+    const int r = base + ((threadIdx.x & 31) >> 2);
+    const int head = static_cast<int>((static_cast<float>(r) + 0.5f) * per_tok);  // r / ntok, r < 2^16
+    const int s = r - head * ntok;
+    const int64_t slot = r < rows ? slot_of[s] : -1;
+    uint4 raw[sizeof(T)][2];  // BF16: [0..1][0..1] are blocks 0..3; FP32: [block][half]
+    const uint4* src = reinterpret_cast<const uint4*>(x + s * p.tok_stride[y] + head * p.head_stride[y]);
 #pragma unroll
-    for (int u = 0; u < kKv4Batch; ++u) {
-      const int r = base + kHalves * u + (hw & 1);
-      row[u] = -1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i >> 2][i & 3] = 0.f;
-      if (r < rows) {
-        const int head = static_cast<int>((static_cast<float>(r) + 0.5f) * per_tok);  // r / ntok, r < 2^16
-        const int s = r - head * ntok;
-        if (slot_of[s] >= 0) {
-          row[u] = kv4_row(p.c, slot_of[s], head);
-          const T* src = x + (tok0 + s) * p.tok_stride[y] + head * p.head_stride[y] + 32 * b0 + 4 * g;
-          kv4_load4<T>(src, v[u][0]);
-          kv4_load4<T>(src + 32, v[u][1]);
-        }
-      }
+    for (int i = 0; i < 2 * static_cast<int>(sizeof(T)); ++i) {
+      raw[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+      if (slot >= 0) raw[i >> 1][i & 1] = __ldg(src + (sizeof(T) == 2 ? 4 * i : 8 * (i >> 1) + (i & 1)));
     }
+    uint32_t h[2][4];  // the four runs of two bytes: [run 2t or 2t + 1][block]
+    uint32_t sf = 0;
 #pragma unroll
-    for (int u = 0; u < kKv4Batch; ++u) {
-      uint32_t codes = 0, sf = 0;
+    for (int b = 0; b < 4; ++b) {
+      float v[8];
+      if (sizeof(T) == 2) {
+        const uint4 u = raw[b >> 1][b & 1];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float amax = fmaxf(fmaxf(fabsf(v[u][b][0]), fabsf(v[u][b][1])), fmaxf(fabsf(v[u][b][2]), fabsf(v[u][b][3])));
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      } else {
+        const uint4 lo = raw[b % sizeof(T)][0], hi = raw[b % sizeof(T)][1];
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int m = 8; m > 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
-        const int e = e8m0_exponent_e2m1(amax, p.floor_mode);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, normal
-        codes |= (cvt_e2m1x2(v[u][b][0] * inv, v[u][b][1] * inv) |
-                  (cvt_e2m1x2(v[u][b][2] * inv, v[u][b][3] * inv) << 8)) << (16 * b);
-        sf |= static_cast<uint32_t>(e + 127) << (8 * b);
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
       }
-      if (row[u] >= 0) {
-        *reinterpret_cast<uint32_t*>(p.c.payload[y] + row[u] * 64 + l16 * 4) = codes;
-        if (l16 < 2) *reinterpret_cast<uint16_t*>(p.c.scales[y] + row[u] * 4 + l16 * 2) = static_cast<uint16_t>(sf);
-      }
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int e = e8m0_exponent_e2m1(amax, p.floor_mode);
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, normal
+      h[0][b] = cvt_e2m1x2(v[0] * inv, v[1] * inv) | (cvt_e2m1x2(v[2] * inv, v[3] * inv) << 8);
+      h[1][b] = cvt_e2m1x2(v[4] * inv, v[5] * inv) | (cvt_e2m1x2(v[6] * inv, v[7] * inv) << 8);
+      sf |= static_cast<uint32_t>(e + 127) << (8 * b);
+    }
+    if (slot >= 0) {
+      const int64_t row = kv4_row(p.c, slot, head);
+      *reinterpret_cast<uint4*>(p.c.payload[y] + row * 64 + t * 16) =
+          make_uint4(h[0][0] | (h[0][1] << 16), h[0][2] | (h[0][3] << 16), h[1][0] | (h[1][1] << 16),
+                     h[1][2] | (h[1][3] << 16));
+      if (t == 0) *reinterpret_cast<uint32_t*>(p.c.scales[y] + row * 4) = sf;
     }
   }
 }
@@ -193,19 +188,19 @@ struct Kv4ReadParams {
   const int32_t* start;
 };
 
-// Grid (16 x padded 128-token blocks, 2): 8 of the 128 rows of a block, rows r0 and r0 + 1 of each
+// Grid (4 x padded 128-token blocks, 2): 32 of the 128 rows of a block, rows r0 .. r0 + 7 of each
 // 32-row quarter, whose scale words fill whole sectors of the atoms.
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
-  __shared__ int64_t slot_of[8];
-  __shared__ int tok_of[8];  // -1: a padding row
-  extern __shared__ __align__(16) uint32_t kv4_sf[];  // [head][8]
-  const int lane = threadIdx.x & 31, l16 = lane & 15, hw = threadIdx.x >> 4;
-  const int block = blockIdx.x >> 4, r0 = (blockIdx.x & 15) * 2;
+  __shared__ int64_t slot_of[kKv4Tile];
+  __shared__ int tok_of[kKv4Tile];  // -1: a padding row
+  extern __shared__ __align__(16) uint32_t kv4_sf[];  // [head][row of the quarter][quarter]
+  const int t = threadIdx.x & 3;
+  const int block = blockIdx.x >> 2, r0 = (blockIdx.x & 3) * 8;
   const int y = blockIdx.y;
-  if (threadIdx.x < 8) {
+  if (threadIdx.x < kKv4Tile) {
     const int seq = find_seq(p.scale_off, p.num_seqs, block);
     const int first = __ldg(p.cu_seqlens + seq);
-    const int in_seq = (block - __ldg(p.scale_off + seq)) * 128 + r0 + (threadIdx.x & 1) + 32 * (threadIdx.x >> 1);
+    const int in_seq = (block - __ldg(p.scale_off + seq)) * 128 + r0 + (threadIdx.x & 7) + 32 * (threadIdx.x >> 3);
     const bool real = in_seq < __ldg(p.cu_seqlens + seq + 1) - first;
     const int start = p.start ? __ldg(p.start + seq) : 0;
     tok_of[threadIdx.x] = real ? first + in_seq : -1;
@@ -213,41 +208,35 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_cons
         real ? kv4_slot(p.c, seq, start >= 0 ? static_cast<int64_t>(start) + in_seq : -1, kKv4ReadSite) : -1;
   }
   __syncthreads();
-  const int g = l16 >> 1, b0 = (l16 & 1) * 2;
-  const int rows = 8 * p.c.heads;
-  constexpr int kHalves = kKv4Threads / 16;
-#pragma unroll 1
-  for (int base = hw; base < rows; base += kHalves * kKv4Batch) {
-    uint32_t codes[kKv4Batch], sf[kKv4Batch];
+  const int rows = kKv4Tile * p.c.heads;
+#pragma unroll 2
+  for (int r = threadIdx.x >> 2; r < rows; r += kKv4Rows) {
+    const int s = r & (kKv4Tile - 1), head = r / kKv4Tile;
+    const int64_t slot = slot_of[s];
+    uint4 codes = make_uint4(0, 0, 0, 0);
+    uint32_t sf = 0x7F7F7F7Fu;
+    if (slot >= 0) {
+      const int64_t row = kv4_row(p.c, slot, head);
+      codes = *reinterpret_cast<const uint4*>(p.c.payload[y] + row * 64 + t * 16);
+      if (t == 0) sf = *reinterpret_cast<const uint32_t*>(p.c.scales[y] + row * 4);
+    }
+    if (tok_of[s] >= 0) {
+      uint8_t* dst = p.payload[y] + (static_cast<int64_t>(tok_of[s]) * p.c.heads + head) * 128 + 8 * t;
+      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-    for (int u = 0; u < kKv4Batch; ++u) {
-      const int r = base + kHalves * u;
-      codes[u] = 0;
-      sf[u] = 0x7F7F7F7Fu;
-      if (r < rows && slot_of[r & 7] >= 0) {
-        const int64_t row = kv4_row(p.c, slot_of[r & 7], r >> 3);
-        codes[u] = *reinterpret_cast<const uint32_t*>(p.c.payload[y] + row * 64 + l16 * 4);
-        if (l16 == 0) sf[u] = *reinterpret_cast<const uint32_t*>(p.c.scales[y] + row * 4);
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t both = __byte_perm(w[b >> 1], w[2 + (b >> 1)], (b & 1) ? 0x7632 : 0x5410);
+        *reinterpret_cast<uint2*>(dst + 32 * b) =
+            make_uint2(e2m1x4_to_e4m3x4(both & 0xFFFFu), e2m1x4_to_e4m3x4(both >> 16));
       }
     }
-#pragma unroll
-    for (int u = 0; u < kKv4Batch; ++u) {
-      const int r = base + kHalves * u;
-      if (r >= rows) break;
-      const int s = r & 7, head = r >> 3;
-      if (tok_of[s] >= 0) {
-        uint8_t* dst = p.payload[y] + (static_cast<int64_t>(tok_of[s]) * p.c.heads + head) * 128 + 32 * b0 + 4 * g;
-        *reinterpret_cast<uint32_t*>(dst) = e2m1x4_to_e4m3x4(codes[u] & 0xFFFFu);
-        *reinterpret_cast<uint32_t*>(dst + 32) = e2m1x4_to_e4m3x4(codes[u] >> 16);
-      }
-      if (l16 == 0) kv4_sf[head * 8 + (s & 1) * 4 + (s >> 1)] = sf[u];
-    }
+    if (t == 0) kv4_sf[head * kKv4Tile + (s & 7) * 4 + (s >> 3)] = sf;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.c.heads; i += kKv4Threads) {
-    const int row = i & 1, head = i >> 1;
+  for (int i = threadIdx.x; i < 8 * p.c.heads; i += kKv4Threads) {
+    const int row = i & 7, head = i >> 3;
     *reinterpret_cast<uint4*>(p.scales[y] + (static_cast<int64_t>(block) * p.c.heads + head) * 512 + (r0 + row) * 16) =
-        *reinterpret_cast<const uint4*>(kv4_sf + head * 8 + row * 4);
+        *reinterpret_cast<const uint4*>(kv4_sf + head * kKv4Tile + row * 4);
   }
 }
 

@@ -833,6 +833,14 @@ lpfa_status rope_setup(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
   return LPFA_OK;
 }
 
+// Whether a warp's four rows are heads of one token (contiguous reads) or one head of four tokens: the
+// latter where the heads left over in steps of four would cost more than a tenth.
+int rope_quad(const lpfa::RopeParams& p) {
+  const int rows = p.t[0].heads + p.t[1].heads;
+  const int steps = (p.t[0].heads + 3) / 4 + (p.t[1].heads + 3) / 4;
+  return 40 * steps <= 11 * rows;
+}
+
 int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
   return !w || heads < 1 ? 0 : (head_stride != 0 ? heads : 1);
 }
@@ -841,7 +849,7 @@ int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
 
 extern "C++" {
 template <int kOut>
-static lpfa_status launch_rope(bool fp32, bool half, unsigned grid, size_t smem, const lpfa::RopeParams& p,
+static lpfa_status launch_rope(bool fp32, bool half, dim3 grid, size_t smem, const lpfa::RopeParams& p,
                                const lpfa::RopePlan& plan, void* stream) {
   auto kernel = fp32 ? (half ? lpfa::qk_norm_rope_kernel<float, kOut, true> : lpfa::qk_norm_rope_kernel<float, kOut, false>)
                      : (half ? lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, true>
@@ -873,10 +881,16 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
   }
   DeviceInfo info;
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
-  // Few tokens: one per block, so that the launch fills the card; else the angles of up to eight
-  // tokens are computed by as many threads as there are.
-  p.tile = static_cast<int>(std::min<int64_t>(lpfa::kRopeTile, (tokens + 4 * info.sms - 1) / (4 * info.sms)));
-  const unsigned grid = static_cast<unsigned>((tokens + p.tile - 1) / p.tile);
+  p.quad = rope_quad(p);
+  const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
+  const unsigned blocks = static_cast<unsigned>((tokens + ntok - 1) / ntok);
+  const int steps = p.quad ? (p.t[0].heads + 3) / 4 + (p.t[1].heads + 3) / 4 : p.t[0].heads + p.t[1].heads;
+  // All heads of a token share its angles; with too few tokens for two blocks per SM the heads are
+  // split (down to two steps a block) to shorten the call.
+  unsigned parts = 1;
+  while (blocks * parts < 2u * info.sms && 2 * static_cast<int>(parts) < steps) parts *= 2;
+  p.steps = (steps + static_cast<int>(parts) - 1) / static_cast<int>(parts);
+  const dim3 grid(blocks, static_cast<unsigned>((steps + p.steps - 1) / p.steps));
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream)
                                 : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream);
@@ -910,10 +924,22 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   DeviceInfo info;
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
-  const size_t smem = static_cast<size_t>(p.t[0].heads + p.t[1].heads) * lpfa::kRopeTile * 4;
-  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half, static_cast<unsigned>(meta->total_scale_blocks) * 16u,
-                                       smem, p, plan, stream);
+  p.quad = rope_quad(p);
+  p.steps = p.t[0].heads + p.t[1].heads;  // all
+  const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
+  const size_t smem = static_cast<size_t>(p.t[0].heads + p.t[1].heads) * ntok * 4;
+  const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * (128u / ntok));
+  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half, grid, smem, p, plan, stream);
 }
+
+extern "C++" {
+template <typename T>
+static auto rope_bwd_kernel(bool half, bool per_head) {
+  return half ? (per_head ? lpfa::qk_norm_rope_bwd_kernel<T, true, true> : lpfa::qk_norm_rope_bwd_kernel<T, true, false>)
+              : (per_head ? lpfa::qk_norm_rope_bwd_kernel<T, false, true>
+                          : lpfa::qk_norm_rope_bwd_kernel<T, false, false>);
+}
+}  // extern "C++"
 
 size_t lpfa_qk_norm_rope_bwd_workspace_bytes(int32_t q_heads, int32_t k_heads, const lpfa_norm_rope* op) {
   if (!op || q_heads < 1 || k_heads < 0) return 0;
@@ -966,16 +992,16 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
   p.tile = static_cast<int>((tokens + lpfa::kRopeBwdBlocks - 1) / lpfa::kRopeBwdBlocks);
   const int blocks = static_cast<int>((tokens + p.tile - 1) / p.tile);
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
-  auto kernel = dt == LPFA_IN_FP32
-                    ? (half ? lpfa::qk_norm_rope_bwd_kernel<float, true> : lpfa::qk_norm_rope_bwd_kernel<float, false>)
-                    : (half ? lpfa::qk_norm_rope_bwd_kernel<__nv_bfloat16, true>
-                            : lpfa::qk_norm_rope_bwd_kernel<__nv_bfloat16, false>);
+  p.quad = rope_quad(p);
+  const bool per_head = p.w_rows[0] > 1 || p.w_rows[1] > 1;
+  auto kernel = dt == LPFA_IN_FP32 ? rope_bwd_kernel<float>(half, per_head)
+                                   : rope_bwd_kernel<__nv_bfloat16>(half, per_head);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   kernel<<<blocks, lpfa::kRopeThreads, 0, s>>>(p, plan);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "norm and rotation backward launch");
   if (rows) {
-    lpfa::qk_norm_rope_dw_kernel<<<rows, 1024, 0, s>>>(p.partials, blocks, rows, p.w_rows[0], dq_weight, dk_weight);
+    lpfa::qk_norm_rope_dw_kernel<<<dim3(rows, 4), 1024, 0, s>>>(p.partials, blocks, rows, p.w_rows[0], dq_weight, dk_weight);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
   }
   return LPFA_OK;
@@ -1041,7 +1067,7 @@ lpfa_status lpfa_kv4_write(const lpfa_rows* k, const lpfa_rows* v, lpfa_in_dtype
   p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
   DeviceInfo info;
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
-  // As for the rotation: a token per block while there are few.
+  // One token per block while there are few, else up to 32 that share their table lookups.
   p.tile = std::min(lpfa::kKv4Tile, (p.tokens + 4 * info.sms - 1) / (4 * info.sms));
   const dim3 grid(static_cast<unsigned>((p.tokens + p.tile - 1) / p.tile), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1075,10 +1101,13 @@ lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* ta
   p.start = start;
   DeviceInfo info;
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
-  const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * 16u, 2);
-  lpfa::kv4_read_kernel<<<grid, lpfa::kKv4Threads, static_cast<size_t>(cache->heads) * 32,
-                          static_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * 4u, 2);
+  const int smem = cache->heads * lpfa::kKv4Tile * 4;  // up to 128 KB
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(lpfa::kv4_read_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  lpfa::kv4_read_kernel<<<grid, lpfa::kKv4Threads, static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)>>>(p);
+  e = cudaGetLastError();
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache read launch");
 }
 

@@ -9,12 +9,14 @@
 //   dw += g * x r,  h = g * w,  dx = r h - x r^3 mean(h x).
 // Everything between the loads and the stores is FP32; a value is rounded once, to its output type.
 //
-// What bounds it: HBM. A row is read once and written once; 16 lanes own a row (8 elements, one
-// 16-byte load of BF16 each), so the norm is four shuffles and an interleaved pair never leaves its
-// lane; a half pair (i, i + 64) is one shuffle with the lane eight away. A warp has two rows at a
-// time and kRopeBatch such pairs of rows in flight. The angles depend on the token alone: a block
-// computes those of its few tokens once, into shared memory, and every head of Q and K reads them.
-// An angle is a product in FP64 reduced to a fraction of a turn by one FMA (exact up to the
+// What bounds it: HBM, once the arithmetic is out of the way; a first version with one element per
+// FP32 instruction and 16 lanes per row needed 79 warp instructions per row and stopped at 64 % of
+// the copy bandwidth. So eight lanes own a row: a lane has elements 8 j .. 8 j + 7 and 64 + 8 j ..
+// 64 + 8 j + 7, whole 16-byte loads that hold complete pairs of either pairing, and all arithmetic
+// is on two floats at a time (f32x2). A warp has four rows, kRopeBatch steps of them in flight. The
+// weight is folded into the rotation (w_a cos, w_b sin, ...) once per token, for all heads. The
+// angles depend on the token alone: a block computes those of its few tokens once, into shared
+// memory. An angle is a product in FP64 reduced to a fraction of a turn by one FMA (exact up to the
 // frequency's own rounding), so far positions keep their accuracy; sincospif does the rest.
 #pragma once
 
@@ -29,11 +31,10 @@ namespace lpfa {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeTile = 8;      // tokens of a forward block (at most)
-constexpr int kRopeBwdTile = 32;  // tokens whose angles a backward block holds at a time
-constexpr int kRopeBatch = 4;     // rows that a half warp has in flight
-// Backward blocks, and with them rows of weight-gradient partials: four for each of 148 SMs.
-constexpr int kRopeBwdBlocks = 592;
+constexpr int kRopeTokens = 4 * kRopeWarps;  // tokens of a forward block, at most
+constexpr int kRopeBwdTile = 64;             // tokens whose angles a backward block holds at a time
+// Backward blocks, and with them rows of weight-gradient partials: two for each of 148 SMs.
+constexpr int kRopeBwdBlocks = 296;
 
 enum RopeOut : int { kRopeBf16 = 0, kRopeF32 = 1, kRopeMxfp8 = 2 };
 
@@ -65,7 +66,9 @@ struct RopeParams {
   int pos64;   // positions are int64 (else int32)
   int w_bf16;  // weights are BF16 (else FP32)
   int norm;
-  int tile;  // forward: tokens per block; backward: tokens per block in all
+  int quad;  // 1: a warp's four rows are heads of one token; 0: the same head of four tokens
+  int tile;  // backward: tokens per block in all
+  int steps; // forward: steps (of four rows) per block and token, of those of Q and K together
   // MXFP8 only
   int num_seqs;
   const int32_t* cu_seqlens;
@@ -76,37 +79,46 @@ struct RopeParams {
   int w_rows[2];  // 0: no weight; 1: one row for all heads; heads: a row each
 };
 
-template <typename T>
-__device__ __forceinline__ void row_load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void row_load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+// Two floats in one register pair, and the arithmetic on them.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
 }
-template <>
-__device__ __forceinline__ void row_load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void f2_get(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  float lo, hi;
+  f2_get(a, lo, hi);
+  return lo + hi;
 }
 
-// A row's 8 elements as they stand in memory: loaded before anything waits for them. Plain loads
-// (not the read-only path): the output may be the input itself.
+// A lane's 16 elements of a row as they stand in memory (chunks at 8 j and 64 + 8 j): loaded before
+// anything waits for them. Plain loads, not the read-only path: the output may be the input itself.
 template <typename T> struct RawRow;
 template <> struct RawRow<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+  uint4 c[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    c[0] = *reinterpret_cast<const uint4*>(p);
+    c[1] = *reinterpret_cast<const uint4*>(p + 64);
   }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  __device__ __forceinline__ void zero() { c[0] = c[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(int k, float (&v)[8]) const {
+    const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(w[i] << 16);
@@ -115,37 +127,100 @@ template <> struct RawRow<__nv_bfloat16> {
   }
 };
 template <> struct RawRow<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    a = s[0];
-    b = s[1];
+  float4 c[4];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4* s = reinterpret_cast<const float4*>(p);
+    c[0] = s[0];
+    c[1] = s[1];
+    c[2] = s[16];
+    c[3] = s[17];
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void zero() { c[0] = c[1] = c[2] = c[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(int k, float (&v)[8]) const {
+    const float4 a = c[2 * k], b = c[2 * k + 1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 };
 
-__device__ __forceinline__ void row_store8(__nv_bfloat16* p, const float (&v)[8]) {
+// The same 16 elements as eight pairs: a[i] holds the first elements of pairs 2 i and 2 i + 1, b[i]
+// the second ones. Pairs: interleaved 4 j .. 4 j + 3 and 32 + 4 j .. 32 + 4 j + 3; half 8 j .. 8 j + 7.
+struct Pairs {
+  F2 a[4], b[4];
+};
+
+template <bool kHalf>
+__device__ __forceinline__ int pair_of(int j, int i) {  // i-th pair (0..7) of lane j
+  return kHalf ? 8 * j + i : 4 * j + (i & 3) + 32 * (i >> 2);
+}
+
+template <bool kHalf>
+__device__ __forceinline__ Pairs to_pairs(const float (&x)[8], const float (&y)[8]) {  // chunks at 8 j, 64 + 8 j
+  Pairs p;
+  if (kHalf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p.a[i] = f2(x[2 * i], x[2 * i + 1]);
+      p.b[i] = f2(y[2 * i], y[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      p.a[i] = f2(x[4 * i], x[4 * i + 2]);
+      p.b[i] = f2(x[4 * i + 1], x[4 * i + 3]);
+      p.a[2 + i] = f2(y[4 * i], y[4 * i + 2]);
+      p.b[2 + i] = f2(y[4 * i + 1], y[4 * i + 3]);
+    }
+  }
+  return p;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void from_pairs(const Pairs& p, float (&x)[8], float (&y)[8]) {
+  if (kHalf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f2_get(p.a[i], x[2 * i], x[2 * i + 1]);
+      f2_get(p.b[i], y[2 * i], y[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f2_get(p.a[i], x[4 * i], x[4 * i + 2]);
+      f2_get(p.b[i], x[4 * i + 1], x[4 * i + 3]);
+      f2_get(p.a[2 + i], y[4 * i], y[4 * i + 2]);
+      f2_get(p.b[2 + i], y[4 * i + 1], y[4 * i + 3]);
+    }
+  }
+}
+
+__device__ __forceinline__ void chunk_store(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
                                             cvt_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ void row_store8(float* p, const float (&v)[8]) {
+__device__ __forceinline__ void chunk_store(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-__device__ __forceinline__ void weight_load8(const RopeParams& p, const RopeTensor& t, int head, int col, float (&w)[8]) {
+template <bool kHalf>
+__device__ __forceinline__ Pairs weight_pairs(const RopeParams& p, const RopeTensor& t, int head, int j) {
+  float x[8], y[8];
   if (t.w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    for (int i = 0; i < 8; ++i) x[i] = y[i] = 1.f;
   } else if (p.w_bf16) {
-    row_load8(static_cast<const __nv_bfloat16*>(t.w) + head * t.w_head + col, w);
+    RawRow<__nv_bfloat16> r;
+    r.load(static_cast<const __nv_bfloat16*>(t.w) + head * t.w_head + 8 * j);
+    r.get(0, x);
+    r.get(1, y);
   } else {
-    row_load8(static_cast<const float*>(t.w) + head * t.w_head + col, w);
+    RawRow<float> r;
+    r.load(static_cast<const float*>(t.w) + head * t.w_head + 8 * j);
+    r.get(0, x);
+    r.get(1, y);
   }
+  return to_pairs<kHalf>(x, y);
 }
 
 // (cos, sin) of token `tok`, pair `pair`.
@@ -161,66 +236,69 @@ __device__ __forceinline__ float2 rope_turn(const RopeParams& p, const RopePlan&
   return cs;
 }
 
-// Sum over the 16 lanes of a row; every lane of the warp takes part.
+// Sum over the 8 lanes of a row; every lane of the warp takes part.
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-  for (int m = 8; m; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  for (int m = 4; m; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
   return v;
 }
 
-// Rotates a lane's 8 elements by cs (of the row's token), or back with kBack.
-template <bool kHalf, bool kBack>
-__device__ __forceinline__ void rotate8(float (&u)[8], const float2* cs, int lane16) {
-  if (kHalf) {
-    // Elements (i, i + 64): lanes 0..7 hold the first of each pair, lanes 8..15 the second.
-    const float4* c4 = reinterpret_cast<const float4*>(cs + (lane16 & 7) * 8);
-    const float sign = (lane16 < 8) != kBack ? -1.f : 1.f;
+// cos and sin of lane j's pairs.
+template <bool kHalf>
+__device__ __forceinline__ void turn_pairs(const float2* cs, int j, F2 (&c)[4], F2 (&s)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 c = c4[i];
-      const float o0 = __shfl_xor_sync(0xFFFFFFFFu, u[2 * i], 8);
-      const float o1 = __shfl_xor_sync(0xFFFFFFFFu, u[2 * i + 1], 8);
-      u[2 * i] = fmaf(u[2 * i], c.x, sign * (o0 * c.y));
-      u[2 * i + 1] = fmaf(u[2 * i + 1], c.z, sign * (o1 * c.w));
-    }
-  } else {
-    const float4* c4 = reinterpret_cast<const float4*>(cs + lane16 * 4);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 c = c4[i];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float co = j ? c.z : c.x;
-        const float si = kBack ? -(j ? c.w : c.y) : (j ? c.w : c.y);
-        const float a = u[4 * i + 2 * j], b = u[4 * i + 2 * j + 1];
-        u[4 * i + 2 * j] = fmaf(a, co, -(b * si));
-        u[4 * i + 2 * j + 1] = fmaf(a, si, b * co);
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(cs + pair_of<kHalf>(j, 2 * i));
+    c[i] = f2(v.x, v.z);
+    s[i] = f2(v.y, v.w);
   }
 }
 
-// Grid: blocks of `tile` tokens (MXFP8: 8 of the 128 rows of a padded block: rows r0, r0 + 1 of each
-// 32-row quarter, which together fill whole sectors of the scale atoms). TIn, kOut, kHalf as named.
+// The rotation with the weight in it: y_a = x_a ac + x_b bs, y_b = x_a as + x_b bc.
+struct Turn {
+  F2 ac[4], bs[4], as[4], bc[4];
+};
+template <bool kHalf>
+__device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs& w, int j) {
+  const F2 minus = f2(-1.f, -1.f);
+  F2 c[4], s[4];
+  turn_pairs<kHalf>(cs, j, c, s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m.ac[i] = f2_mul(w.a[i], c[i]);
+    m.as[i] = f2_mul(w.a[i], s[i]);
+    m.bc[i] = f2_mul(w.b[i], c[i]);
+    m.bs[i] = f2_mul(f2_mul(w.b[i], s[i]), minus);
+  }
+}
+
+// Grid (token blocks, head parts). A warp's four rows are four heads of one token (quad) or, for few
+// heads, one head of four tokens; a step is four rows, and blockIdx.y takes p.steps of the steps of Q
+// and K. A block has 8 (32) tokens: consecutive ones, or for MXFP8 the rows r0, r0 + 1 (.. r0 + 7) of
+// each 32-row quarter of a padded 128-token block, which together fill whole sectors of the scale
+// atoms.
 template <typename TIn, int kOut, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads)
 qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
-  __shared__ __align__(16) float2 cs[kRopeTile][64];
-  __shared__ int64_t tok_of[kRopeTile];  // -1: no such token
-  extern __shared__ __align__(16) uint32_t sf_words[];  // MXFP8: [Q and K head][8 rows], the rows' four scale bytes
+  constexpr int kBatch = sizeof(TIn) == 2 ? 2 : 1;  // steps that a warp loads before it computes
+  __shared__ __align__(16) float2 cs[kRopeTokens][64];
+  __shared__ int64_t tok_of[kRopeTokens];  // -1: no such token
+  extern __shared__ __align__(16) uint32_t sf_words[];  // MXFP8: [Q and K head][token], the four scale bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half = lane >> 4, l16 = lane & 15;
-  int64_t atom0 = 0;  // MXFP8: 128-token block, and the first row of this tile in its quarter
+  const int grp = lane >> 3, j = lane & 7;
+  const int ntok = p.quad ? kRopeWarps : kRopeTokens;
+  const int span = ntok / 4;  // MXFP8: rows of a quarter
+  int64_t atom0 = 0;          // MXFP8: the 128-token block, and the first row of this tile in a quarter
   int r0 = 0;
-  const int ntok = kOut == kRopeMxfp8 ? kRopeTile : p.tile;
 
   if (kOut == kRopeMxfp8) {
-    atom0 = blockIdx.x >> 4;
-    r0 = (blockIdx.x & 15) * 2;
-    if (threadIdx.x < kRopeTile) {
+    const int parts = 32 / span;
+    atom0 = blockIdx.x / parts;
+    r0 = (blockIdx.x % parts) * span;
+    if (threadIdx.x < ntok) {
       const int seq = find_seq(p.scale_off, p.num_seqs, static_cast<int>(atom0));
       const int start = __ldg(p.cu_seqlens + seq);
-      const int64_t in_seq = (atom0 - __ldg(p.scale_off + seq)) * 128 + r0 + (threadIdx.x & 1) + 32 * (threadIdx.x >> 1);
+      const int64_t in_seq = (atom0 - __ldg(p.scale_off + seq)) * 128 + r0 + threadIdx.x % span + 32 * (threadIdx.x / span);
       tok_of[threadIdx.x] = in_seq < __ldg(p.cu_seqlens + seq + 1) - start ? start + in_seq : -1;
     }
   } else if (threadIdx.x < ntok) {
@@ -234,228 +312,314 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   }
   __syncthreads();
 
+  const int slot = p.quad ? warp : warp * 4 + grp;
+  const int64_t tok = tok_of[slot];
+  const int heads_per_step = p.quad ? 4 : 1;
+  const int head0 = p.quad ? grp : 0;  // of this lane's row within a step
+  const float2* my_cs = cs[tok >= 0 ? slot : 0];
+  int lo = blockIdx.y * p.steps, hi = lo + p.steps;  // steps of this block, Q's first, then K's
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const RopeTensor& t = p.t[which];
-    if (t.heads == 0) continue;
-    const int rows = ntok * t.heads;
-    const float per_head = 1.f / static_cast<float>(t.heads);
-    float w[8];
-    weight_load8(p, t, 0, l16 * 8, w);
+    const int steps = (t.heads + heads_per_step - 1) / heads_per_step;
+    const int s0 = max(lo, 0), s1 = min(hi, steps);
+    lo -= steps;
+    hi -= steps;
+    if (s0 >= s1) continue;
+    Turn m;
+    {
+      const Pairs w = weight_pairs<kHalf>(p, t, 0, j);
+      make_turn<kHalf>(m, my_cs, w, j);
+    }
+    const TIn* src = static_cast<const TIn*>(t.x) + (tok >= 0 ? tok : 0) * t.tok_stride + 8 * j;
 #pragma unroll 1
-    for (int base = 2 * warp; base < rows; base += 2 * kRopeWarps * kRopeBatch) {
-      RawRow<TIn> raw[kRopeBatch];
-      int64_t tok[kRopeBatch];
-      int slot[kRopeBatch], head[kRopeBatch];
+    for (int st = s0; st < s1; st += kBatch) {
+      RawRow<TIn> raw[kBatch];
 #pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int r = base + 2 * kRopeWarps * u + half;
-        // r / heads: r + 1/2 keeps the product off the whole numbers (r < 2^16).
-        slot[u] = static_cast<int>((static_cast<float>(r) + 0.5f) * per_head);
-        head[u] = r - slot[u] * t.heads;
-        tok[u] = r < rows ? tok_of[slot[u]] : -2;  // -2: beyond the tile, -1: a padding row
-        if (tok[u] >= 0)
-          raw[u].load(t.x, tok[u] * t.tok_stride + head[u] * t.head_stride + l16 * 8);
+      for (int u = 0; u < kBatch; ++u) {
+        const int head = (st + u) * heads_per_step + head0;
+        if (tok >= 0 && st + u < s1 && head < t.heads)
+          raw[u].load(src + head * t.head_stride);
         else
           raw[u].zero();
       }
 #pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        if (base + 2 * kRopeWarps * u >= rows) break;  // the same for the whole warp
-        float v[8];
-        raw[u].get(v);
-        if (p.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-          const float r = rsqrtf(row_sum(ss) * (1.f / 128.f) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= r;
+      for (int u = 0; u < kBatch; ++u) {
+        if (st + u >= s1) break;  // the same for the whole warp
+        const int head = (st + u) * heads_per_step + head0;
+        const bool real = head < t.heads;
+        if (t.w_head != 0) {
+          const Pairs w = weight_pairs<kHalf>(p, t, real ? head : 0, j);
+          make_turn<kHalf>(m, my_cs, w, j);
         }
-        if (t.w_head != 0) weight_load8(p, t, head[u], l16 * 8, w);
+        float x[8], y[8];
+        raw[u].get(0, x);
+        raw[u].get(1, y);
+        Pairs v = to_pairs<kHalf>(x, y);
+        F2 r = f2(1.f, 1.f);
+        if (p.norm) {
+          F2 ss = f2_mul(v.a[0], v.a[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= w[i];
-        rotate8<kHalf, false>(v, cs[tok[u] >= 0 ? slot[u] : 0], l16);
+          for (int i = 1; i < 4; ++i) ss = f2_fma(v.a[i], v.a[i], ss);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = f2_fma(v.b[i], v.b[i], ss);
+          const float inv = rsqrtf(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
+          r = f2(inv, inv);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 a = f2_mul(v.a[i], r), b = f2_mul(v.b[i], r);
+          v.a[i] = f2_fma(a, m.ac[i], f2_mul(b, m.bs[i]));
+          v.b[i] = f2_fma(a, m.as[i], f2_mul(b, m.bc[i]));
+        }
+        from_pairs<kHalf>(v, x, y);
         if (kOut == kRopeMxfp8) {
-          // The quantizer's rule (quantize.cuh): a 32-element block is four lanes.
-          float amax = 0.f;
+          // The quantizer's rule (quantize.cuh): a 32-element block is a chunk of four lanes.
+          uint8_t* dst = static_cast<uint8_t*>(t.out) + ((tok >= 0 ? tok : 0) * t.heads + head) * 128 + 8 * j;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-          const int e = e8m0_exponent(amax, p.floor_mode);
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          if (tok[u] >= 0) {
-            const uint32_t w0 = cvt_e4m3x2(v[0] * inv, v[1] * inv) |
-                                (static_cast<uint32_t>(cvt_e4m3x2(v[2] * inv, v[3] * inv)) << 16);
-            const uint32_t w1 = cvt_e4m3x2(v[4] * inv, v[5] * inv) |
-                                (static_cast<uint32_t>(cvt_e4m3x2(v[6] * inv, v[7] * inv)) << 16);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.out) + (tok[u] * t.heads + head[u]) * 128 + l16 * 8) =
-                make_uint2(w0, w1);
+          for (int k = 0; k < 2; ++k) {
+            float(&z)[8] = k ? y : x;
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(z[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const int e = e8m0_exponent(amax, p.floor_mode);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (tok >= 0 && real)
+              *reinterpret_cast<uint2*>(dst + 64 * k) =
+                  make_uint2(cvt_e4m3x2(z[0] * inv, z[1] * inv) |
+                                 (static_cast<uint32_t>(cvt_e4m3x2(z[2] * inv, z[3] * inv)) << 16),
+                             cvt_e4m3x2(z[4] * inv, z[5] * inv) |
+                                 (static_cast<uint32_t>(cvt_e4m3x2(z[6] * inv, z[7] * inv)) << 16));
+            if (real && (j & 3) == 0)  // rows of one quarter side by side: [head][row of the quarter][quarter]
+              reinterpret_cast<uint8_t*>(sf_words + ((which ? p.t[0].heads : 0) + head) * ntok +
+                                         (slot % span) * 4 + slot / span)[2 * k + (j >> 2)] =
+                  tok >= 0 ? static_cast<uint8_t>(e + 127) : uint8_t{0x7F};
           }
-          if (tok[u] >= -1 && (l16 & 3) == 0)
-            reinterpret_cast<uint8_t*>(sf_words + ((which ? p.t[0].heads : 0) + head[u]) * kRopeTile +
-                                       (slot[u] & 1) * 4 + (slot[u] >> 1))[l16 >> 2] =
-                tok[u] >= 0 ? static_cast<uint8_t>(e + 127) : uint8_t{0x7F};
-        } else if (tok[u] >= 0) {
-          const int64_t at = tok[u] * t.out_tok + head[u] * t.out_head + l16 * 8;
-          if (kOut == kRopeBf16)
-            row_store8(static_cast<__nv_bfloat16*>(t.out) + at, v);
-          else
-            row_store8(static_cast<float*>(t.out) + at, v);
+        } else if (tok >= 0 && real) {
+          const int64_t at = tok * t.out_tok + head * t.out_head + 8 * j;
+          if (kOut == kRopeBf16) {
+            chunk_store(static_cast<__nv_bfloat16*>(t.out) + at, x);
+            chunk_store(static_cast<__nv_bfloat16*>(t.out) + at + 64, y);
+          } else {
+            chunk_store(static_cast<float*>(t.out) + at, x);
+            chunk_store(static_cast<float*>(t.out) + at + 64, y);
+          }
         }
       }
     }
   }
   if (kOut == kRopeMxfp8) {
-    // Row r0 + j of the four quarters: 16 contiguous bytes of the head's atom.
+    // The four quarters of row r0 + row: 16 contiguous bytes of the head's atom. (One head part.)
     __syncthreads();
     const int hq = p.t[0].heads;
-    for (int i = threadIdx.x; i < 2 * (hq + p.t[1].heads); i += kRopeThreads) {
-      const int row = i & 1, h = i >> 1;
+    for (int i = threadIdx.x; i < span * (hq + p.t[1].heads); i += kRopeThreads) {
+      const int row = i % span, h = i / span;
       const RopeTensor& t = p.t[h >= hq];
       const int head = h >= hq ? h - hq : h;
       *reinterpret_cast<uint4*>(t.scales + (atom0 * t.heads + head) * 512 + (r0 + row) * 16) =
-          *reinterpret_cast<const uint4*>(sf_words + h * kRopeTile + row * 4);
+          *reinterpret_cast<const uint4*>(sf_words + h * ntok + row * 4);
     }
   }
 }
 
-// Backward. Each block walks `tile` consecutive tokens, kRopeBwdTile at a time. A half warp keeps
-// one head while it walks tokens, so the weight gradient of its 8 channels stays in registers: one
-// sum over everything it saw (one weight row), or one per head, added to the block's own row of
-// partials. No atomics: the same sums in the same order every time.
-template <typename T, bool kHalf>
+// Backward. Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, each warp its own
+// tokens and for each all heads (steps of four rows as in the forward pass, the next one's loads
+// under way while one is computed). With one weight row for all heads a lane's sums for its 16
+// channels stay in registers to the end. With a row per head a warp keeps a step's heads while it
+// walks the tokens, and the warps' sums go through shared memory to the block's own row of partials.
+// No atomics: the same sums in the same order every time.
+template <typename T, bool kHalf, bool kPerHead>
 __global__ void __launch_bounds__(kRopeThreads)
 qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
-  constexpr int kHalves = 2 * kRopeWarps;
-  constexpr int kBatch = 2;
   __shared__ __align__(16) float2 cs[kRopeBwdTile][64];
-  __shared__ __align__(16) float sums[kHalves][128];
-  const int lane = threadIdx.x & 31, l16 = lane & 15;
-  const int hw = threadIdx.x >> 4;  // half warp
+  __shared__ __align__(16) float sums[4 * kRopeWarps][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane >> 3, j = lane & 7;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int64_t last = min(first + p.tile, p.tokens);
   const int part_rows = p.w_rows[0] + p.w_rows[1];
   float* part = p.partials + static_cast<int64_t>(blockIdx.x) * part_rows * 128;
+  const int heads_per_step = p.quad ? 4 : 1;
+  const int head0 = p.quad ? grp : 0;
+  const int tok_step = p.quad ? kRopeWarps : 4 * kRopeWarps;
+  const int tok_first = p.quad ? warp : warp * 4;  // of the warp; the lane's own: + (quad ? 0 : grp)
+  const F2 minus = f2(-1.f, -1.f);
 
-  float acc[2][8];
+  // One weight row: the warps' sums join here. (Rows and channels of `sums` as the lanes hold them.)
+  auto put_sums = [&](const F2 (&acc)[8]) {
+    Pairs v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      v.a[i] = acc[i];
+      v.b[i] = acc[4 + i];
+    }
+    float x[8], y[8];
+    from_pairs<kHalf>(v, x, y);
+    chunk_store(&sums[warp * 4 + grp][8 * j], x);
+    chunk_store(&sums[warp * 4 + grp][64 + 8 * j], y);
+  };
 
-  for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
-    const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
-    __syncthreads();  // the angles of the previous tokens have been read
-    for (int i = threadIdx.x; i < ntok * 64; i += kRopeThreads)
-      cs[i >> 6][i & 63] = rope_turn(p, plan, tok0 + (i >> 6), i & 63);
-    __syncthreads();
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const RopeTensor& t = p.t[which];
-      const bool per_head = p.w_rows[which] > 1;
 #pragma unroll 1
-      for (int h0 = 0; h0 < t.heads; h0 += kHalves) {
-        // nh heads on the half warps, `groups` half warps sharing the tokens of each.
-        const int nh = min(kHalves, t.heads - h0);
-        const int groups = kHalves / nh;
-        const int grp = hw / nh;
-        const int head = h0 + hw - grp * nh;
-        float w[8];
-        weight_load8(p, t, t.w_head ? head : 0, l16 * 8, w);
+  for (int which = 0; which < 2; ++which) {
+    const RopeTensor& t = p.t[which];
+    if (t.heads == 0) continue;
+    const int steps = (t.heads + heads_per_step - 1) / heads_per_step;
+    F2 acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
+    Pairs w = weight_pairs<kHalf>(p, t, 0, j);
+    for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
+      const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
+      if (which == 0 || last - first > kRopeBwdTile) {  // else Q's angles are still there
+        __syncthreads();                                // the angles of the previous tokens have been read
+        for (int i = threadIdx.x; i < ntok * 64; i += kRopeThreads)
+          cs[i >> 6][i & 63] = rope_turn(p, plan, tok0 + (i >> 6), i & 63);
+        __syncthreads();
+      }
+      // Items of a warp: (token, step) pairs, steps fastest (per head: tokens fastest).
+      const int mine = tok_first < ntok ? (ntok - tok_first + tok_step - 1) / tok_step : 0;
 #pragma unroll 1
-        for (int s0 = 0; s0 < ntok; s0 += kBatch * groups) {
-          RawRow<T> rx[kBatch], rd[kBatch];
-          bool on[kBatch];
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int s = s0 + u * groups + grp;
-            on[u] = grp < groups && s < ntok;
-            if (on[u]) {
-              rx[u].load(t.x, (tok0 + s) * t.tok_stride + head * t.head_stride + l16 * 8);
-              rd[u].load(t.dy, (tok0 + s) * t.dy_tok + head * t.dy_head + l16 * 8);
-            } else {
-              rx[u].zero();
-              rd[u].zero();
-            }
+      for (int outer = 0; outer < (kPerHead ? steps : 1); ++outer) {
+        const int items = kPerHead ? mine : mine * steps;
+        RawRow<T> nx, ng;
+        auto load = [&](int s, int head) {  // s: token of the tile
+          if (s < ntok && head < t.heads) {
+            nx.load(static_cast<const T*>(t.x) + (tok0 + s) * t.tok_stride + head * t.head_stride + 8 * j);
+            ng.load(static_cast<const T*>(t.dy) + (tok0 + s) * t.dy_tok + head * t.dy_head + 8 * j);
+          } else {
+            nx.zero();
+            ng.zero();
           }
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int s = s0 + u * groups + grp;
-            float x[8], g[8];
-            rx[u].get(x);
-            rd[u].get(g);
-            rotate8<kHalf, true>(g, cs[on[u] ? s : 0], l16);
-            float r = 1.f, m = 0.f;
-            if (p.norm) {
-              float ss = 0.f, hx = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                ss = fmaf(x[i], x[i], ss);
-                hx = fmaf(g[i] * w[i], x[i], hx);
-              }
-              ss = row_sum(ss);
-              hx = row_sum(hx);
-              r = rsqrtf(ss * (1.f / 128.f) + p.eps);
-              m = hx * (1.f / 128.f) * r * r;
-            }
-            float dx[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dx[i] = r * (g[i] * w[i] - x[i] * m);
-              acc[which][i] = fmaf(g[i], x[i] * r, acc[which][i]);  // zero rows add nothing
-            }
-            if (on[u]) row_store8(static_cast<T*>(t.out) + (tok0 + s) * t.out_tok + head * t.out_head + l16 * 8, dx);
+        };
+        int step = kPerHead ? outer : 0;
+        int s = tok_first + (p.quad ? 0 : grp);
+        if (items > 0) load(s, step * heads_per_step + head0);
+        if (kPerHead && t.w_head != 0)
+          w = weight_pairs<kHalf>(p, t, min(step * heads_per_step + head0, t.heads - 1), j);
+        F2 c[4], sn[4];
+        if (!kPerHead && items > 0) turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
+#pragma unroll 1
+        for (int it = 0; it < items; ++it) {
+          const int head = step * heads_per_step + head0;
+          const int now = s;
+          const bool on = now < ntok && head < t.heads;
+          const RawRow<T> rx = nx, rg = ng;
+          if (kPerHead) turn_pairs<kHalf>(cs[min(now, ntok - 1)], j, c, sn);
+          // Next item.
+          bool new_token = true;
+          if (kPerHead) {
+            s += tok_step;
+          } else if (++step == steps) {
+            step = 0;
+            s += tok_step;
+          } else {
+            new_token = false;
           }
+          if (it + 1 < items) load(s, step * heads_per_step + head0);
+
+          float u[8], v[8];
+          rg.get(0, u);
+          rg.get(1, v);
+          Pairs g = to_pairs<kHalf>(u, v);
+          rx.get(0, u);
+          rx.get(1, v);
+          const Pairs x = to_pairs<kHalf>(u, v);
+          F2 ss = f2(0.f, 0.f), hx = f2(0.f, 0.f);
+          F2 gx[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // Back by the angle: g_a = dy_a c + dy_b s, g_b = dy_b c - dy_a s.
+            const F2 a = f2_fma(g.a[i], c[i], f2_mul(g.b[i], sn[i]));
+            const F2 b = f2_fma(g.b[i], c[i], f2_mul(f2_mul(g.a[i], minus), sn[i]));
+            g.a[i] = a;
+            g.b[i] = b;
+            gx[i] = f2_mul(a, x.a[i]);
+            gx[4 + i] = f2_mul(b, x.b[i]);
+            hx = f2_fma(gx[i], w.a[i], hx);
+            hx = f2_fma(gx[4 + i], w.b[i], hx);
+            ss = f2_fma(x.a[i], x.a[i], ss);
+            ss = f2_fma(x.b[i], x.b[i], ss);
+          }
+          float r = 1.f, q = 0.f;  // dx = r g w + q x
+          if (p.norm) {
+            r = rsqrtf(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
+            q = row_sum(f2_sum(hx)) * (-1.f / 128.f) * r * r * r;
+          }
+          const F2 r2 = f2(r, r), q2 = f2(q, q);
+          Pairs d;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[i] = f2_fma(gx[i], r2, acc[i]);  // rows that do not exist add 0
+            acc[4 + i] = f2_fma(gx[4 + i], r2, acc[4 + i]);
+            d.a[i] = f2_fma(f2_mul(g.a[i], w.a[i]), r2, f2_mul(x.a[i], q2));
+            d.b[i] = f2_fma(f2_mul(g.b[i], w.b[i]), r2, f2_mul(x.b[i], q2));
+          }
+          if (on) {
+            from_pairs<kHalf>(d, u, v);
+            T* dst = static_cast<T*>(t.out) + (tok0 + now) * t.out_tok + head * t.out_head + 8 * j;
+            chunk_store(dst, u);
+            chunk_store(dst + 64, v);
+          }
+          if (!kPerHead && new_token && it + 1 < items) turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
         }
-        if (per_head) {
-          // The block's sum for these heads, over the half warps that shared each.
+        if (kPerHead && p.w_rows[which] > 1) {
+          put_sums(acc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sums[hw][l16 * 8 + i] = acc[which][i];
-            acc[which][i] = 0.f;
-          }
+          for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
           __syncthreads();
-          for (int i = threadIdx.x; i < nh * 128; i += kRopeThreads) {
-            float s = 0.f;
-            for (int g = 0; g < groups; ++g) s += sums[g * nh + (i >> 7)][i & 127];
-            float* to = part + (which * p.w_rows[0] + h0) * 128 + i;
-            *to = tok0 == first ? s : *to + s;
+          for (int i = threadIdx.x; i < heads_per_step * 128; i += kRopeThreads) {
+            const int head = outer * heads_per_step + (i >> 7);
+            if (head >= t.heads) continue;
+            float sum = 0.f;
+            if (p.quad) {
+#pragma unroll
+              for (int k = 0; k < kRopeWarps; ++k) sum += sums[4 * k + (i >> 7)][i & 127];
+            } else {
+              for (int k = 0; k < 4 * kRopeWarps; ++k) sum += sums[k][i];
+            }
+            float* to = part + (which * p.w_rows[0] + head) * 128 + (i & 127);
+            *to = tok0 == first ? sum : *to + sum;
           }
           __syncthreads();
         }
       }
     }
-  }
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (p.w_rows[which] != 1) continue;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[hw][l16 * 8 + i] = acc[which][i];
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      float s = 0.f;
-      for (int g = 0; g < kHalves; ++g) s += sums[g][threadIdx.x];
-      part[which * p.w_rows[0] * 128 + threadIdx.x] = s;
+    if (p.w_rows[which] == 1) {
+      __syncthreads();
+      put_sums(acc);
+      __syncthreads();
+      if (threadIdx.x < 128) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < 4 * kRopeWarps; ++k) sum += sums[k][threadIdx.x];
+        part[which * p.w_rows[0] * 128 + threadIdx.x] = sum;
+      }
     }
   }
 }
 
-// Sums the blocks' partial weight gradients: one block of 8 x 128 threads for a row of the result.
+// Sums the blocks' partial weight gradients. Grid (rows, 4): 32 channels of a row of the result for
+// a block of 32 x 32 threads, so that a thread has few loads to wait for and all at once.
 __global__ void __launch_bounds__(1024)
 qk_norm_rope_dw_kernel(const float* partials, int blocks, int rows, int rows_q, float* dwq, float* dwk) {
-  __shared__ float sums[8][128];
-  const int row = blockIdx.x, ch = threadIdx.x & 127, grp = threadIdx.x >> 7;
+  __shared__ float sums[32][33];
+  const int row = blockIdx.x, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int ch = blockIdx.y * 32 + lane;
   float s = 0.f;
-#pragma unroll 8
-  for (int b = grp; b < blocks; b += 8) s += __ldg(partials + (static_cast<int64_t>(b) * rows + row) * 128 + ch);
-  sums[grp][ch] = s;
-  __syncthreads();
-  if (grp == 0) {
 #pragma unroll
-    for (int g = 1; g < 8; ++g) s += sums[g][ch];
-    (row < rows_q ? dwq + row * 128 : dwk + (row - rows_q) * 128)[ch] = s;
+  for (int i = 0; i < (kRopeBwdBlocks + 31) / 32; ++i) {
+    const int b = grp + 32 * i;
+    if (b < blocks) s += __ldg(partials + (static_cast<int64_t>(b) * rows + row) * 128 + ch);
   }
+  sums[grp][lane] = s;
+  __syncthreads();
+  // Warp g sums channel g of the 32 over the groups.
+  s = sums[lane][grp];
+#pragma unroll
+  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+  if (lane == 0) (row < rows_q ? dwq + row * 128 : dwk + (row - rows_q) * 128)[blockIdx.y * 32 + grp] = s;
 }
 
 }  // namespace lpfa
