@@ -849,12 +849,12 @@ int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
 
 extern "C++" {
 template <int kOut>
-static lpfa_status launch_rope(bool fp32, bool half, dim3 grid, size_t smem, const lpfa::RopeParams& p,
+static lpfa_status launch_rope(bool fp32, bool half, dim3 grid, const lpfa::RopeParams& p,
                                const lpfa::RopePlan& plan, void* stream) {
   auto kernel = fp32 ? (half ? lpfa::qk_norm_rope_kernel<float, kOut, true> : lpfa::qk_norm_rope_kernel<float, kOut, false>)
                      : (half ? lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, true>
                              : lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, false>);
-  kernel<<<grid, lpfa::kRopeThreads, smem, static_cast<cudaStream_t>(stream)>>>(p, plan);
+  kernel<<<grid, lpfa::kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, plan);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation launch");
 }
@@ -883,17 +883,18 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
   p.quad = rope_quad(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
-  const unsigned blocks = static_cast<unsigned>((tokens + ntok - 1) / ntok);
+  p.tiles = static_cast<int>((tokens + ntok - 1) / ntok);
   const int steps = p.quad ? (p.t[0].heads + 3) / 4 + (p.t[1].heads + 3) / 4 : p.t[0].heads + p.t[1].heads;
-  // All heads of a token share its angles; with too few tokens for two blocks per SM the heads are
-  // split (down to two steps a block) to shorten the call.
-  unsigned parts = 1;
-  while (blocks * parts < 2u * info.sms && 2 * static_cast<int>(parts) < steps) parts *= 2;
-  p.steps = (steps + static_cast<int>(parts) - 1) / static_cast<int>(parts);
-  const dim3 grid(blocks, static_cast<unsigned>((steps + p.steps - 1) / p.steps));
+  // Two blocks per SM walk the tiles. All heads of a token share its angles; with fewer tiles than
+  // blocks the heads are split (down to two steps a block) to shorten the call.
+  const int slots = 2 * info.sms;
+  int parts = 1;
+  while (p.tiles * parts < slots && 2 * parts < steps) parts *= 2;
+  p.steps = (steps + parts - 1) / parts;
+  const dim3 grid(static_cast<unsigned>(std::min(p.tiles, slots)), static_cast<unsigned>((steps + p.steps - 1) / p.steps));
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
-  return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream)
-                                : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, 0, p, plan, stream);
+  return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, p, plan, stream)
+                                : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, p, plan, stream);
 }
 
 lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int32_t head_dim,
@@ -927,9 +928,9 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   p.quad = rope_quad(p);
   p.steps = p.t[0].heads + p.t[1].heads;  // all
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
-  const size_t smem = static_cast<size_t>(p.t[0].heads + p.t[1].heads) * ntok * 4;
-  const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * (128u / ntok));
-  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half, grid, smem, p, plan, stream);
+  p.tiles = meta->total_scale_blocks * (128 / ntok);
+  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half,
+                                       dim3(static_cast<unsigned>(std::min(p.tiles, 2 * info.sms))), p, plan, stream);
 }
 
 extern "C++" {

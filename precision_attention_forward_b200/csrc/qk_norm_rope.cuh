@@ -67,6 +67,7 @@ struct RopeParams {
   int w_bf16;  // weights are BF16 (else FP32)
   int norm;
   int quad;  // 1: a warp's four rows are heads of one token; 0: the same head of four tokens
+  int tiles; // forward: tiles of tokens
   int tile;  // backward: tokens per block in all
   int steps; // forward: steps (of four rows) per block and token, of those of Q and K together
   // MXFP8 only
@@ -80,31 +81,26 @@ struct RopeParams {
 };
 
 // Two floats in one register pair, and the arithmetic on them.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
+typedef float2 F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float f2_sum(F2 a) { return a.x + a.y; }
 __device__ __forceinline__ void f2_get(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+  lo = a.x;
+  hi = a.y;
 }
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+// max(a, |b|, |c|) for a >= 0, and max over a chunk's 8 magnitudes.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ float f2_sum(F2 a) {
-  float lo, hi;
-  f2_get(a, lo, hi);
-  return lo + hi;
+__device__ __forceinline__ float chunk_amax(const float (&v)[8]) {
+  float m = max3_abs(v[0], v[1], v[2]);
+  m = max3_abs(m, v[3], v[4]);
+  m = max3_abs(m, v[5], v[6]);
+  return fmaxf(m, fabsf(v[7]));
 }
 
 // A lane's 16 elements of a row as they stand in memory (chunks at 8 j and 64 + 8 j): loaded before
@@ -223,17 +219,46 @@ __device__ __forceinline__ Pairs weight_pairs(const RopeParams& p, const RopeTen
   return to_pairs<kHalf>(x, y);
 }
 
-// (cos, sin) of token `tok`, pair `pair`.
-__device__ __forceinline__ float2 rope_turn(const RopeParams& p, const RopePlan& plan, int64_t tok, int pair) {
-  if (p.pos == nullptr) return make_float2(1.f, 0.f);  // no rotation
-  const int64_t at = tok * p.pos_tok + plan.axis[pair] * p.pos_axis;
-  const double pos = p.pos64 ? static_cast<double>(__ldg(static_cast<const long long*>(p.pos) + at))
-                             : static_cast<double>(__ldg(static_cast<const int*>(p.pos) + at));
-  const double f = plan.turns[pair];
-  const float frac = static_cast<float>(fma(pos, f, -rint(pos * f)));  // in [-1/2, 1/2] of a turn
-  float2 cs;
-  sincospif(2.f * frac, &cs.y, &cs.x);
-  return cs;
+// The rotations that a lane computes, those of pairs `lane` and `lane + 32`: read once (a lane's own
+// entries of the kernel's constants are a serialised read, 13 us of the video forward when it was
+// done for every token).
+struct LaneTurns {
+  double f[2];
+  int64_t axis[2];  // offsets in the position row
+};
+__device__ __forceinline__ LaneTurns lane_turns(const RopeParams& p, const RopePlan& plan, int lane) {
+  LaneTurns r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.f[i] = plan.turns[lane + 32 * i];
+    r.axis[i] = plan.axis[lane + 32 * i] * p.pos_axis;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int64_t rope_position(const RopeParams& p, int64_t at) {
+  if (p.pos == nullptr) return 0;
+  return p.pos64 ? __ldg(static_cast<const long long*>(p.pos) + at) : __ldg(static_cast<const int*>(p.pos) + at);
+}
+
+// (cos, sin) of position n at f turns a step.
+__device__ __forceinline__ float2 rope_turn(int64_t n, double f) {
+  const double pos = static_cast<double>(n);
+  // Quarter turns, and a rest in [-1/8, 1/8] of a turn whose FP32 rounding is below 2^-28.
+  const double quarters = rint(pos * f * 4.0);
+  const float rest = static_cast<float>(fma(pos, f, -0.25 * quarters));
+  float s, c;
+  sincospif(2.f * rest, &s, &c);
+  const int q = static_cast<int>(static_cast<long long>(quarters)) & 3;
+  const float co = (q & 1) ? s : c, si = (q & 1) ? c : s;
+  return make_float2((q == 1 || q == 2) ? -co : co, q >= 2 ? -si : si);
+}
+
+// 1 / sqrt(v): the approximation and one Newton step.
+__device__ __forceinline__ float rsqrt_newton(float v) {
+  const float r = rsqrtf(v);
+  const float e = fmaf(-v * r, r, 1.f);
+  return v > 0.f && r < INFINITY && v < INFINITY ? fmaf(0.5f * r, e, r) : r;
 }
 
 // Sum over the 8 lanes of a row; every lane of the warp takes part.
@@ -272,84 +297,153 @@ __device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs
   }
 }
 
-// Grid (token blocks, head parts). A warp's four rows are four heads of one token (quad) or, for few
-// heads, one head of four tokens; a step is four rows, and blockIdx.y takes p.steps of the steps of Q
-// and K. A block has 8 (32) tokens: consecutive ones, or for MXFP8 the rows r0, r0 + 1 (.. r0 + 7) of
-// each 32-row quarter of a padded 128-token block, which together fill whole sectors of the scale
-// atoms.
+// Grid (blocks, head parts). A warp's four rows are four heads of one token (quad) or, for few heads,
+// one head of four tokens; a step is four rows, and blockIdx.y takes p.steps of the steps of Q and
+// then K. Tiles of 8 (32) tokens go round the blocks: consecutive tokens, or for MXFP8 the rows r0,
+// r0 + 1 (.. r0 + 7) of each 32-row quarter of a padded 128-token block, whose scale words fill whole
+// sectors of the atoms between them. The warps are on their own, without a barrier: each computes its
+// tokens' angles while its first rows are on the way, and loads ahead into its next token.
 template <typename TIn, int kOut, bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
-  constexpr int kBatch = sizeof(TIn) == 2 ? 2 : 1;  // steps that a warp loads before it computes
+  constexpr int kBatch = sizeof(TIn) == 2 ? 2 : 1;  // steps that a warp loads ahead of the one it computes
   __shared__ __align__(16) float2 cs[kRopeTokens][64];
-  __shared__ int64_t tok_of[kRopeTokens];  // -1: no such token
-  extern __shared__ __align__(16) uint32_t sf_words[];  // MXFP8: [Q and K head][token], the four scale bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
   const int ntok = p.quad ? kRopeWarps : kRopeTokens;
-  const int span = ntok / 4;  // MXFP8: rows of a quarter
-  int64_t atom0 = 0;          // MXFP8: the 128-token block, and the first row of this tile in a quarter
-  int r0 = 0;
+  const int slot = p.quad ? warp : warp * 4 + grp;  // this lane's token of a tile
+  const int span = ntok / 4;                        // MXFP8: rows of a quarter
+  const int parts = 32 / span;                      // MXFP8: tiles of a 128-token block
+  const int in_block = slot % span + 32 * (slot / span);
+  const float2* my_cs = cs[slot];
 
-  if (kOut == kRopeMxfp8) {
-    const int parts = 32 / span;
-    atom0 = blockIdx.x / parts;
-    r0 = (blockIdx.x % parts) * span;
-    if (threadIdx.x < ntok) {
-      const int seq = find_seq(p.scale_off, p.num_seqs, static_cast<int>(atom0));
+  struct Place {
+    int64_t tok;     // token; 0 where there is none (read the first, write nothing)
+    int64_t block;   // MXFP8: 128-token block, and the row in it
+    int row;
+    bool real;
+  };
+  auto place = [&](int tile) {
+    Place w;
+    w.block = 0;
+    w.row = 0;
+    if (kOut == kRopeMxfp8) {
+      w.block = tile / parts;
+      w.row = (tile % parts) * span + in_block;
+      const int seq = find_seq(p.scale_off, p.num_seqs, static_cast<int>(w.block));
       const int start = __ldg(p.cu_seqlens + seq);
-      const int64_t in_seq = (atom0 - __ldg(p.scale_off + seq)) * 128 + r0 + threadIdx.x % span + 32 * (threadIdx.x / span);
-      tok_of[threadIdx.x] = in_seq < __ldg(p.cu_seqlens + seq + 1) - start ? start + in_seq : -1;
+      const int64_t in_seq = (w.block - __ldg(p.scale_off + seq)) * 128 + w.row;
+      w.tok = start + in_seq;
+      w.real = in_seq < __ldg(p.cu_seqlens + seq + 1) - start;
+    } else {
+      w.tok = static_cast<int64_t>(tile) * ntok + slot;
+      w.real = w.tok < p.tokens;
     }
-  } else if (threadIdx.x < ntok) {
-    const int64_t tok = static_cast<int64_t>(blockIdx.x) * ntok + threadIdx.x;
-    tok_of[threadIdx.x] = tok < p.tokens ? tok : -1;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < ntok * 64; i += kRopeThreads) {
-    const int64_t tok = tok_of[i >> 6];
-    if (tok >= 0) cs[i >> 6][i & 63] = rope_turn(p, plan, tok, i & 63);
-  }
-  __syncthreads();
+    if (!w.real) w.tok = 0;
+    return w;
+  };
 
-  const int slot = p.quad ? warp : warp * 4 + grp;
-  const int64_t tok = tok_of[slot];
   const int heads_per_step = p.quad ? 4 : 1;
   const int head0 = p.quad ? grp : 0;  // of this lane's row within a step
-  const float2* my_cs = cs[tok >= 0 ? slot : 0];
-  int lo = blockIdx.y * p.steps, hi = lo + p.steps;  // steps of this block, Q's first, then K's
+  const int steps_q = (p.t[0].heads + heads_per_step - 1) / heads_per_step;
+  const int steps_k = (p.t[1].heads + heads_per_step - 1) / heads_per_step;
+  const int s0 = blockIdx.y * p.steps;
+  const int s1 = min(steps_q + steps_k, s0 + p.steps);
+
+  // A head that does not exist reads the last one; what it gives is not stored.
+  const TIn *row_q, *row_k;
+  RawRow<TIn> next[kBatch];
+  auto rows_of = [&](int64_t tok) {
+    row_q = static_cast<const TIn*>(p.t[0].x) + tok * p.t[0].tok_stride + 8 * j;
+    row_k = static_cast<const TIn*>(p.t[1].x) + tok * p.t[1].tok_stride + 8 * j;
+  };
+  auto load = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int g = first + u;
+      if (g < steps_q && g < s1)
+        next[u].load(row_q + min(g * heads_per_step + head0, p.t[0].heads - 1) * p.t[0].head_stride);
+      else if (g < s1)
+        next[u].load(row_k + min((g - steps_q) * heads_per_step + head0, p.t[1].heads - 1) * p.t[1].head_stride);
+    }
+  };
+  int tile = blockIdx.x;
+  if (tile >= p.tiles) return;
+  Place now = place(tile);
+  rows_of(now.tok);
+  load(s0);
+  const LaneTurns turns = lane_turns(p, plan, lane);
+  int64_t ahead[2];  // positions of the warp's (quad: next) token
+#pragma unroll
+  for (int i = 0; i < 2; ++i) ahead[i] = p.quad ? rope_position(p, now.tok * p.pos_tok + turns.axis[i]) : 0;
+
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const RopeTensor& t = p.t[which];
-    const int steps = (t.heads + heads_per_step - 1) / heads_per_step;
-    const int s0 = max(lo, 0), s1 = min(hi, steps);
-    lo -= steps;
-    hi -= steps;
-    if (s0 >= s1) continue;
+  for (; tile < p.tiles; tile += gridDim.x) {
+    // The angles of the warp's tokens.
+    __syncwarp();  // the previous ones have been read
+#pragma unroll 1
+    for (int of = 0; of < (p.quad ? 1 : 4); ++of) {
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, now.tok, of * 8);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t n = p.quad ? ahead[i] : rope_position(p, at * p.pos_tok + turns.axis[i]);
+        cs[(p.quad ? warp : warp * 4) + of][lane + 32 * i] = rope_turn(n, turns.f[i]);
+      }
+    }
+    __syncwarp();
+    // The next tile: its rows' first loads follow this one's last.
+    const bool more = tile + static_cast<int>(gridDim.x) < p.tiles;
+    const Place after = more ? place(tile + gridDim.x) : now;
+    if (p.quad && more) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ahead[i] = rope_position(p, after.tok * p.pos_tok + turns.axis[i]);
+    }
+
+    // The tensor that the steps have come to.
     Turn m;
-    {
+    int heads = 0, head = 0;
+    bool per_head = false;
+    uint8_t *sf = nullptr, *bytes = nullptr;
+    __nv_bfloat16* out16 = nullptr;
+    float* out32 = nullptr;
+    int64_t out_step = 0;
+    auto enter = [&](int which, int step) {
+      const RopeTensor& t = p.t[which];
       const Pairs w = weight_pairs<kHalf>(p, t, 0, j);
       make_turn<kHalf>(m, my_cs, w, j);
-    }
-    const TIn* src = static_cast<const TIn*>(t.x) + (tok >= 0 ? tok : 0) * t.tok_stride + 8 * j;
+      heads = t.heads;
+      per_head = t.w_head != 0;
+      head = step * heads_per_step + head0;
+      // Where this lane's row goes: values, or payload bytes and its scale bytes.
+      if (kOut == kRopeMxfp8) {
+        sf = t.scales + (now.block * heads + head) * 512 + (now.row & 31) * 16 + (now.row >> 5) * 4;
+        bytes = static_cast<uint8_t*>(t.out) + (now.tok * heads + head) * 128 + 8 * j;
+      } else if (kOut == kRopeBf16) {
+        out16 = static_cast<__nv_bfloat16*>(t.out) + now.tok * t.out_tok + head * t.out_head + 8 * j;
+      } else {
+        out32 = static_cast<float*>(t.out) + now.tok * t.out_tok + head * t.out_head + 8 * j;
+      }
+      out_step = heads_per_step * t.out_head;
+    };
+    if (s0 < steps_q) enter(0, s0);
 #pragma unroll 1
     for (int st = s0; st < s1; st += kBatch) {
       RawRow<TIn> raw[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int head = (st + u) * heads_per_step + head0;
-        if (tok >= 0 && st + u < s1 && head < t.heads)
-          raw[u].load(src + head * t.head_stride);
-        else
-          raw[u].zero();
+      for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
+      if (st + kBatch < s1) {
+        load(st + kBatch);
+      } else if (more) {
+        rows_of(after.tok);
+        load(s0);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (st + u >= s1) break;  // the same for the whole warp
-        const int head = (st + u) * heads_per_step + head0;
-        const bool real = head < t.heads;
-        if (t.w_head != 0) {
-          const Pairs w = weight_pairs<kHalf>(p, t, real ? head : 0, j);
+        if (st + u == steps_q || heads == 0) enter(1, st + u - steps_q);
+        const bool real = now.real && head < heads;
+        if (per_head) {
+          const Pairs w = weight_pairs<kHalf>(p, p.t[st + u >= steps_q], min(head, heads - 1), j);
           make_turn<kHalf>(m, my_cs, w, j);
         }
         float x[8], y[8];
@@ -363,7 +457,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
           for (int i = 1; i < 4; ++i) ss = f2_fma(v.a[i], v.a[i], ss);
 #pragma unroll
           for (int i = 0; i < 4; ++i) ss = f2_fma(v.b[i], v.b[i], ss);
-          const float inv = rsqrtf(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
+          const float inv = rsqrt_newton(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
           r = f2(inv, inv);
         }
 #pragma unroll
@@ -375,52 +469,49 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
         from_pairs<kHalf>(v, x, y);
         if (kOut == kRopeMxfp8) {
           // The quantizer's rule (quantize.cuh): a 32-element block is a chunk of four lanes.
-          uint8_t* dst = static_cast<uint8_t*>(t.out) + ((tok >= 0 ? tok : 0) * t.heads + head) * 128 + 8 * j;
+          uint32_t sfw = 0;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float(&z)[8] = k ? y : x;
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(z[i]));
+            float amax = chunk_amax(z);
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
             const int e = e8m0_exponent(amax, p.floor_mode);
             const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            if (tok >= 0 && real)
-              *reinterpret_cast<uint2*>(dst + 64 * k) =
-                  make_uint2(cvt_e4m3x2(z[0] * inv, z[1] * inv) |
-                                 (static_cast<uint32_t>(cvt_e4m3x2(z[2] * inv, z[3] * inv)) << 16),
-                             cvt_e4m3x2(z[4] * inv, z[5] * inv) |
-                                 (static_cast<uint32_t>(cvt_e4m3x2(z[6] * inv, z[7] * inv)) << 16));
-            if (real && (j & 3) == 0)  // rows of one quarter side by side: [head][row of the quarter][quarter]
-              reinterpret_cast<uint8_t*>(sf_words + ((which ? p.t[0].heads : 0) + head) * ntok +
-                                         (slot % span) * 4 + slot / span)[2 * k + (j >> 2)] =
-                  tok >= 0 ? static_cast<uint8_t>(e + 127) : uint8_t{0x7F};
+            const F2 inv2 = f2(inv, inv);
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const F2 q = f2_mul(f2(z[2 * i], z[2 * i + 1]), inv2);
+              c[i] = cvt_e4m3x2(q.x, q.y);
+            }
+            if (real)
+              *reinterpret_cast<uint2*>(bytes + 64 * k) =
+                  make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+            sfw |= static_cast<uint32_t>(e + 127) << (16 * k);
           }
-        } else if (tok >= 0 && real) {
-          const int64_t at = tok * t.out_tok + head * t.out_head + 8 * j;
-          if (kOut == kRopeBf16) {
-            chunk_store(static_cast<__nv_bfloat16*>(t.out) + at, x);
-            chunk_store(static_cast<__nv_bfloat16*>(t.out) + at + 64, y);
-          } else {
-            chunk_store(static_cast<float*>(t.out) + at, x);
-            chunk_store(static_cast<float*>(t.out) + at + 64, y);
+          // Blocks 0, 2 are lanes 0 .. 3's, 1, 3 lanes 4 .. 7's.
+          sfw |= __shfl_xor_sync(0xFFFFFFFFu, sfw, 4) << 8;
+          if (j == 0 && head < heads) *reinterpret_cast<uint32_t*>(sf) = now.real ? sfw : 0x7F7F7F7Fu;
+          sf += heads_per_step * 512;
+          bytes += heads_per_step * 128;
+        } else if (kOut == kRopeBf16) {
+          if (real) {
+            chunk_store(out16, x);
+            chunk_store(out16 + 64, y);
           }
+          out16 += out_step;
+        } else {
+          if (real) {
+            chunk_store(out32, x);
+            chunk_store(out32 + 64, y);
+          }
+          out32 += out_step;
         }
+        head += heads_per_step;
       }
     }
-  }
-  if (kOut == kRopeMxfp8) {
-    // The four quarters of row r0 + row: 16 contiguous bytes of the head's atom. (One head part.)
-    __syncthreads();
-    const int hq = p.t[0].heads;
-    for (int i = threadIdx.x; i < span * (hq + p.t[1].heads); i += kRopeThreads) {
-      const int row = i % span, h = i / span;
-      const RopeTensor& t = p.t[h >= hq];
-      const int head = h >= hq ? h - hq : h;
-      *reinterpret_cast<uint4*>(t.scales + (atom0 * t.heads + head) * 512 + (r0 + row) * 16) =
-          *reinterpret_cast<const uint4*>(sf_words + h * ntok + row * 4);
-    }
+    now = after;
   }
 }
 
@@ -431,7 +522,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
 // walks the tokens, and the warps' sums go through shared memory to the block's own row of partials.
 // No atomics: the same sums in the same order every time.
 template <typename T, bool kHalf, bool kPerHead>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
   __shared__ __align__(16) float2 cs[kRopeBwdTile][64];
   __shared__ __align__(16) float sums[4 * kRopeWarps][128];
@@ -446,6 +537,8 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
   const int tok_step = p.quad ? kRopeWarps : 4 * kRopeWarps;
   const int tok_first = p.quad ? warp : warp * 4;  // of the warp; the lane's own: + (quad ? 0 : grp)
   const F2 minus = f2(-1.f, -1.f);
+
+  const LaneTurns turns = lane_turns(p, plan, lane);
 
   // One weight row: the warps' sums join here. (Rows and channels of `sums` as the lanes hold them.)
   auto put_sums = [&](const F2 (&acc)[8]) {
@@ -472,30 +565,31 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
     Pairs w = weight_pairs<kHalf>(p, t, 0, j);
     for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
       const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
-      if (which == 0 || last - first > kRopeBwdTile) {  // else Q's angles are still there
-        __syncthreads();                                // the angles of the previous tokens have been read
-        for (int i = threadIdx.x; i < ntok * 64; i += kRopeThreads)
-          cs[i >> 6][i & 63] = rope_turn(p, plan, tok0 + (i >> 6), i & 63);
-        __syncthreads();
-      }
+      if (last - first > kRopeBwdTile) __syncthreads();  // the angles of the previous tokens have been read
       // Items of a warp: (token, step) pairs, steps fastest (per head: tokens fastest).
       const int mine = tok_first < ntok ? (ntok - tok_first + tok_step - 1) / tok_step : 0;
 #pragma unroll 1
       for (int outer = 0; outer < (kPerHead ? steps : 1); ++outer) {
         const int items = kPerHead ? mine : mine * steps;
         RawRow<T> nx, ng;
-        auto load = [&](int s, int head) {  // s: token of the tile
-          if (s < ntok && head < t.heads) {
-            nx.load(static_cast<const T*>(t.x) + (tok0 + s) * t.tok_stride + head * t.head_stride + 8 * j);
-            ng.load(static_cast<const T*>(t.dy) + (tok0 + s) * t.dy_tok + head * t.dy_head + 8 * j);
-          } else {
-            nx.zero();
-            ng.zero();
-          }
+        // Token s of the tile; what does not exist reads the last one there is and counts for nothing.
+        auto load = [&](int s, int head) {
+          const int64_t at = tok0 + min(s, ntok - 1);
+          const int h = min(head, t.heads - 1);
+          nx.load(static_cast<const T*>(t.x) + at * t.tok_stride + h * t.head_stride + 8 * j);
+          ng.load(static_cast<const T*>(t.dy) + at * t.dy_tok + h * t.dy_head + 8 * j);
         };
         int step = kPerHead ? outer : 0;
         int s = tok_first + (p.quad ? 0 : grp);
         if (items > 0) load(s, step * heads_per_step + head0);
+        if (outer == 0 && (which == 0 || last - first > kRopeBwdTile)) {  // else Q's angles are still there
+          for (int s = warp; s < ntok; s += kRopeWarps) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              cs[s][lane + 32 * i] = rope_turn(rope_position(p, (tok0 + s) * p.pos_tok + turns.axis[i]), turns.f[i]);
+          }
+          __syncthreads();
+        }
         if (kPerHead && t.w_head != 0)
           w = weight_pairs<kHalf>(p, t, min(step * heads_per_step + head0, t.heads - 1), j);
         F2 c[4], sn[4];
@@ -544,15 +638,16 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           }
           float r = 1.f, q = 0.f;  // dx = r g w + q x
           if (p.norm) {
-            r = rsqrtf(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
+            r = rsqrt_newton(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
             q = row_sum(f2_sum(hx)) * (-1.f / 128.f) * r * r * r;
           }
           const F2 r2 = f2(r, r), q2 = f2(q, q);
+          const F2 ra = on ? r2 : f2(0.f, 0.f);
           Pairs d;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            acc[i] = f2_fma(gx[i], r2, acc[i]);  // rows that do not exist add 0
-            acc[4 + i] = f2_fma(gx[4 + i], r2, acc[4 + i]);
+            acc[i] = f2_fma(gx[i], ra, acc[i]);
+            acc[4 + i] = f2_fma(gx[4 + i], ra, acc[4 + i]);
             d.a[i] = f2_fma(f2_mul(g.a[i], w.a[i]), r2, f2_mul(x.a[i], q2));
             d.b[i] = f2_fma(f2_mul(g.b[i], w.b[i]), r2, f2_mul(x.b[i], q2));
           }
