@@ -66,14 +66,6 @@ struct Attn4Params {
   float* lse;          // (heads_q, Tq)
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
 // Two E2M1 codes (a byte) -> f16x2, exactly.
 template <int kByte>
 __device__ __forceinline__ uint32_t cvt_e2m1x2_to_f16x2(uint32_t w) {

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
+#include "qk_norm_rope.cuh"
 #include "quantize.cuh"
 
 namespace lpfa {
@@ -68,21 +69,22 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Cache& c, int64_t slot, int 
   return (((slot >> c.page_shift) * c.heads + head) << c.page_shift) + (slot & (c.page_size - 1));
 }
 
-// Two floats -> two E2M1 codes (round to nearest even, saturate to +-6); lo in bits 0..3.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+// Four floats -> four E2M1 codes (round to nearest even, saturate to +-6), the first in bits 0..3.
+__device__ __forceinline__ uint32_t cvt_e2m1x4(F2 a, F2 b) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 lo, hi;\n\tcvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n\tmov.b16 %0, {lo, hi};\n\t}"
+      : "=h"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 
-// E8M0 exponent for E2M1 (6 = 1.5 * 2^2) of a non-negative float block maximum.
-__device__ __forceinline__ int e8m0_exponent_e2m1(float amax, int floor_mode) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int biased = static_cast<int>(bits >> 23);
-  if (biased == 0) return -127;  // zero or subnormal: below 2^-126, clamps to -127
-  const int e = biased - 129 + (!floor_mode && (bits & 0x7FFFFFu) > 0x400000u);
-  return max(-127, min(127, e));
+// Scale byte for E2M1 (6 = 1.5 * 2^2) of a block maximum: e + 127 with e the smallest with
+// amax <= 6 * 2^e (`up` carries a mantissa above 1.5 into the exponent) or, with up 0,
+// floor(log2 amax) - 2; a zero or subnormal maximum gives 0, the clamp at 2^-127.
+__device__ __forceinline__ uint32_t e2m1_scale_byte(float amax, uint32_t up) {
+  return max((__float_as_uint(amax) + up) >> 23, 2u) - 2u;
 }
+constexpr uint32_t kE2m1Up = 0x3FFFFFu;
 
 // Four E2M1 codes (nibbles 0..3) -> four E4M3 codes, exactly.
 __device__ __forceinline__ uint32_t e2m1x4_to_e4m3x4(uint32_t nibbles) {
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const __grid_con
   const T* x = static_cast<const T*>(p.x[y]) + tok0 * p.tok_stride[y] + 8 * t;
   const int rows = ntok * p.c.heads;
   const float per_tok = 1.f / static_cast<float>(ntok);
+  const uint32_t up = p.floor_mode ? 0u : kE2m1Up;
 #pragma unroll 1
   for (int base = (threadIdx.x >> 5) * 8; base < rows; base += kKv4Rows) {  // the same for the whole warp
     const int r = base + ((threadIdx.x & 31) >> 2);
@@ -157,16 +160,18 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
       }
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      float amax = chunk_amax(v);
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int e = e8m0_exponent_e2m1(amax, p.floor_mode);
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, normal
-      h[0][b] = cvt_e2m1x2(v[0] * inv, v[1] * inv) | (cvt_e2m1x2(v[2] * inv, v[3] * inv) << 8);
-      h[1][b] = cvt_e2m1x2(v[4] * inv, v[5] * inv) | (cvt_e2m1x2(v[6] * inv, v[7] * inv) << 8);
-      sf |= static_cast<uint32_t>(e + 127) << (8 * b);
+      const uint32_t byte = e2m1_scale_byte(amax, up);
+      const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e, normal
+      const F2 inv2 = f2(inv, inv);
+      F2 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = f2_mul(f2(v[2 * i], v[2 * i + 1]), inv2);
+      h[0][b] = cvt_e2m1x4(q[0], q[1]);
+      h[1][b] = cvt_e2m1x4(q[2], q[3]);
+      sf |= byte << (8 * b);
     }
     if (slot >= 0) {
       const int64_t row = kv4_row(p.c, slot, head);

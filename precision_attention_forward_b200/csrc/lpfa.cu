@@ -833,12 +833,15 @@ lpfa_status rope_setup(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
   return LPFA_OK;
 }
 
-// Whether a warp's four rows are heads of one token (contiguous reads) or one head of four tokens: the
-// latter where the heads left over in steps of four would cost more than a tenth.
-int rope_quad(const lpfa::RopeParams& p) {
-  const int rows = p.t[0].heads + p.t[1].heads;
-  const int steps = (p.t[0].heads + 3) / 4 + (p.t[1].heads + 3) / 4;
-  return 40 * steps <= 11 * rows;
+// Whether a warp's four rows are heads of one token (contiguous reads), or one head of four tokens:
+// the former where every head then has its place.
+int rope_quad(const lpfa::RopeParams& p) { return p.t[0].heads % 4 == 0 && p.t[1].heads % 4 == 0; }
+
+int rope_batches(const lpfa::RopeParams& p) {
+  const int per_step = p.quad ? 4 : 1;
+  int n = 0;
+  for (const lpfa::RopeTensor& t : p.t) n += (t.heads / per_step + lpfa::kRopeBatch - 1) / lpfa::kRopeBatch;
+  return n;
 }
 
 int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
@@ -854,8 +857,11 @@ static lpfa_status launch_rope(bool fp32, bool half, dim3 grid, const lpfa::Rope
   auto kernel = fp32 ? (half ? lpfa::qk_norm_rope_kernel<float, kOut, true> : lpfa::qk_norm_rope_kernel<float, kOut, false>)
                      : (half ? lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, true>
                              : lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, false>);
-  kernel<<<grid, lpfa::kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, plan);
-  const cudaError_t e = cudaGetLastError();
+  const int smem = fp32 ? lpfa::rope_smem_bytes<float>() : lpfa::rope_smem_bytes<__nv_bfloat16>();
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  kernel<<<grid, lpfa::kRopeThreads, static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)>>>(p, plan);
+  e = cudaGetLastError();
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation launch");
 }
 }  // extern "C++"
@@ -884,14 +890,15 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
   p.quad = rope_quad(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
   p.tiles = static_cast<int>((tokens + ntok - 1) / ntok);
-  const int steps = p.quad ? (p.t[0].heads + 3) / 4 + (p.t[1].heads + 3) / 4 : p.t[0].heads + p.t[1].heads;
   // Two blocks per SM walk the tiles. All heads of a token share its angles; with fewer tiles than
-  // blocks the heads are split (down to two steps a block) to shorten the call.
+  // blocks the heads are split to shorten the call.
   const int slots = 2 * info.sms;
+  const int batches = rope_batches(p);
   int parts = 1;
-  while (p.tiles * parts < slots && 2 * parts < steps) parts *= 2;
-  p.steps = (steps + parts - 1) / parts;
-  const dim3 grid(static_cast<unsigned>(std::min(p.tiles, slots)), static_cast<unsigned>((steps + p.steps - 1) / p.steps));
+  while (p.tiles * parts < slots && parts < batches) parts *= 2;
+  p.batches = (batches + parts - 1) / parts;
+  const dim3 grid(static_cast<unsigned>(std::min(p.tiles, slots)),
+                  static_cast<unsigned>((batches + p.batches - 1) / p.batches));
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, p, plan, stream)
                                 : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, p, plan, stream);
@@ -926,7 +933,7 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   p.quad = rope_quad(p);
-  p.steps = p.t[0].heads + p.t[1].heads;  // all
+  p.batches = rope_batches(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
   p.tiles = meta->total_scale_blocks * (128 / ntok);
   return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half,

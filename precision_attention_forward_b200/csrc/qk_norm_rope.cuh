@@ -32,6 +32,16 @@ namespace lpfa {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeTokens = 4 * kRopeWarps;  // tokens of a forward block, at most
+constexpr int kRopeBatch = 2;                // forward steps that a warp takes together
+// Batches of a warp's shared-memory ring (2 KB each for BF16 input, 4 KB for FP32): one computed, one on
+// the way. More of them are slower: with four (three) the video forward took 151 instead of 132 us and
+// the ragged FP32 to MXFP8 one 272 instead of 258, since the warps' tokens lie apart in memory and
+// each keeps more places of it open.
+template <typename T> constexpr int rope_stages() { return 2; }
+template <typename T> constexpr int rope_stage_bytes() { return kRopeBatch * 4 * 128 * static_cast<int>(sizeof(T)); }
+template <typename T> constexpr int rope_smem_bytes() {
+  return kRopeTokens * 64 * 8 + kRopeWarps * rope_stages<T>() * rope_stage_bytes<T>();
+}
 constexpr int kRopeBwdTile = 64;             // tokens whose angles a backward block holds at a time
 // Backward blocks, and with them rows of weight-gradient partials: two for each of 148 SMs.
 constexpr int kRopeBwdBlocks = 296;
@@ -69,7 +79,7 @@ struct RopeParams {
   int quad;  // 1: a warp's four rows are heads of one token; 0: the same head of four tokens
   int tiles; // forward: tiles of tokens
   int tile;  // backward: tokens per block in all
-  int steps; // forward: steps (of four rows) per block and token, of those of Q and K together
+  int batches; // forward: batches of steps (of four rows) per block and token, of those of Q and K together
   // MXFP8 only
   int num_seqs;
   const int32_t* cu_seqlens;
@@ -103,6 +113,33 @@ __device__ __forceinline__ float chunk_amax(const float (&v)[8]) {
   return fmaxf(m, fabsf(v[7]));
 }
 
+// Scale byte for a block maximum, the bits of e8m0_exponent(amax, floor_mode) + 127: `up` carries a
+// mantissa above 1.75 into the exponent (RCEIL) or is 0 (FLOOR); 448 = 1.75 * 2^8.
+__device__ __forceinline__ uint32_t e4m3_scale_byte(float amax, uint32_t up) {
+  return max((__float_as_uint(amax) + up) >> 23, 8u) - 8u;
+}
+constexpr uint32_t kE4m3Up = 0x1FFFFFu;
+
+// Four floats -> four E4M3 codes (round to nearest even, saturate to +-448).
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void lds16(uint4& v, uint32_t at) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+}
+
 // A lane's 16 elements of a row as they stand in memory (chunks at 8 j and 64 + 8 j): loaded before
 // anything waits for them. Plain loads, not the read-only path: the output may be the input itself.
 template <typename T> struct RawRow;
@@ -112,7 +149,10 @@ template <> struct RawRow<__nv_bfloat16> {
     c[0] = *reinterpret_cast<const uint4*>(p);
     c[1] = *reinterpret_cast<const uint4*>(p + 64);
   }
-  __device__ __forceinline__ void zero() { c[0] = c[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load_shared(uint32_t at, int lane) {
+    lds16(c[0], at + lane * 16);
+    lds16(c[1], at + 512 + lane * 16);
+  }
   __device__ __forceinline__ void get(int k, float (&v)[8]) const {
     const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
 #pragma unroll
@@ -131,7 +171,18 @@ template <> struct RawRow<float> {
     c[2] = s[16];
     c[3] = s[17];
   }
-  __device__ __forceinline__ void zero() { c[0] = c[1] = c[2] = c[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  // (pieces 2 j, 2 j + 1, 16 + 2 j, 17 + 2 j of the row, where those of odd runs have changed places)
+  __device__ __forceinline__ void load_shared(uint32_t at, int lane) {
+    const int j = lane & 7;
+    at += (lane >> 3) * 512;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 u;
+      const int piece = (i >> 1) * 16 + 2 * j + (i & 1);
+      lds16(u, at + (piece ^ ((piece >> 3) & 1)) * 16);
+      c[i] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    }
+  }
   __device__ __forceinline__ void get(int k, float (&v)[8]) const {
     const float4 a = c[2 * k], b = c[2 * k + 1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -258,7 +309,7 @@ __device__ __forceinline__ float2 rope_turn(int64_t n, double f) {
 __device__ __forceinline__ float rsqrt_newton(float v) {
   const float r = rsqrtf(v);
   const float e = fmaf(-v * r, r, 1.f);
-  return v > 0.f && r < INFINITY && v < INFINITY ? fmaf(0.5f * r, e, r) : r;
+  return e == e ? fmaf(0.5f * r, e, r) : r;  // (0 and infinity: r is right as it is)
 }
 
 // Sum over the 8 lanes of a row; every lane of the warp takes part.
@@ -298,16 +349,19 @@ __device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs
 }
 
 // Grid (blocks, head parts). A warp's four rows are four heads of one token (quad) or, for few heads,
-// one head of four tokens; a step is four rows, and blockIdx.y takes p.steps of the steps of Q and
-// then K. Tiles of 8 (32) tokens go round the blocks: consecutive tokens, or for MXFP8 the rows r0,
+// one head of four tokens; a step is four rows, and blockIdx.y takes p.batches of the batches of Q's
+// steps and then K's. Tiles of 8 (32) tokens go round the blocks: consecutive tokens, or for MXFP8 the rows r0,
 // r0 + 1 (.. r0 + 7) of each 32-row quarter of a padded 128-token block, whose scale words fill whole
 // sectors of the atoms between them. The warps are on their own, without a barrier: each computes its
 // tokens' angles while its first rows are on the way, and loads ahead into its next token.
 template <typename TIn, int kOut, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
-  constexpr int kBatch = sizeof(TIn) == 2 ? 2 : 1;  // steps that a warp loads ahead of the one it computes
-  __shared__ __align__(16) float2 cs[kRopeTokens][64];
+  constexpr int kBatch = kRopeBatch;
+  constexpr int kStages = rope_stages<TIn>();
+  constexpr int kStageBytes = rope_stage_bytes<TIn>();
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
   const int ntok = p.quad ? kRopeWarps : kRopeTokens;
@@ -345,63 +399,90 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
 
   const int heads_per_step = p.quad ? 4 : 1;
   const int head0 = p.quad ? grp : 0;  // of this lane's row within a step
-  const int steps_q = (p.t[0].heads + heads_per_step - 1) / heads_per_step;
-  const int steps_k = (p.t[1].heads + heads_per_step - 1) / heads_per_step;
-  const int s0 = blockIdx.y * p.steps;
-  const int s1 = min(steps_q + steps_k, s0 + p.steps);
+  // Batches of kBatch steps, Q's first, then K's; the last one of a tensor may have one step only.
+  // (quad: the heads of both are multiples of four)
+  const int steps_of[2] = {p.t[0].heads / heads_per_step, p.t[1].heads / heads_per_step};
+  const int batches_q = (steps_of[0] + kBatch - 1) / kBatch;
+  const int b0 = blockIdx.y * p.batches;
+  const int b1 = min(batches_q + (steps_of[1] + kBatch - 1) / kBatch, b0 + p.batches);
 
-  // A head that does not exist reads the last one; what it gives is not stored.
-  const TIn *row_q, *row_k;
-  RawRow<TIn> next[kBatch];
-  auto rows_of = [&](int64_t tok) {
-    row_q = static_cast<const TIn*>(p.t[0].x) + tok * p.t[0].tok_stride + 8 * j;
-    row_k = static_cast<const TIn*>(p.t[1].x) + tok * p.t[1].tok_stride + 8 * j;
+  // The loads run ahead, batch after batch and tile after tile, into the warp's ring.
+  const uint32_t ring = smem_u32(rope_smem) + kRopeTokens * 64 * 8 + warp * kStages * kStageBytes;
+  constexpr int kLaneElems = sizeof(TIn) == 2 ? 8 : 4;  // elements of a copy
+  int rd_tile = blockIdx.x, rd_batch = b0, rd_left = 0;
+  uint32_t rd_stage = 0;
+  int64_t rd_tok = 0, rd_step = 0;
+  const TIn* rd = nullptr;
+  auto rd_enter = [&](int which, int step) {
+    const RopeTensor& t = p.t[which];
+    rd = static_cast<const TIn*>(t.x) + rd_tok * t.tok_stride + (step * heads_per_step + head0) * t.head_stride + kLaneElems * j;
+    rd_step = heads_per_step * t.head_stride;
+    rd_left = steps_of[which] - step;
   };
-  auto load = [&](int first) {
+  auto rd_start = [&](int64_t tok) {
+    rd_tok = tok;
+    rd_batch = b0;
+    if (b0 < batches_q) rd_enter(0, b0 * kBatch); else rd_enter(1, (b0 - batches_q) * kBatch);
+  };
+  auto issue = [&]() {
+    if (rd_tile < p.tiles) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int g = first + u;
-      if (g < steps_q && g < s1)
-        next[u].load(row_q + min(g * heads_per_step + head0, p.t[0].heads - 1) * p.t[0].head_stride);
-      else if (g < s1)
-        next[u].load(row_k + min((g - steps_q) * heads_per_step + head0, p.t[1].heads - 1) * p.t[1].head_stride);
+      for (int u = 0; u < kBatch; ++u) {
+        if (u < rd_left) {
+          const uint32_t dst = ring + rd_stage + u * (kStageBytes / kBatch);
+          if (sizeof(TIn) == 2) {
+            cp_async16(dst + lane * 16, rd, 16);
+            cp_async16(dst + 512 + lane * 16, rd + 64, 16);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)  // 128 contiguous bytes of a row each: 16-byte piece 8 c + j
+              cp_async16(dst + grp * 512 + (c * 8 + (j ^ (c & 1))) * 16, rd + 32 * c, 16);
+          }
+          rd += rd_step;
+        }
+      }
+      rd_left -= kBatch;
+      rd_stage = rd_stage + kStageBytes == kStages * kStageBytes ? 0 : rd_stage + kStageBytes;
+      if (++rd_batch == b1) {
+        rd_tile += gridDim.x;
+        if (rd_tile < p.tiles) rd_start(place(rd_tile).tok);
+      } else if (rd_batch == batches_q) {
+        rd_enter(1, 0);
+      }
     }
+    cp_async_commit();
   };
-  int tile = blockIdx.x;
-  if (tile >= p.tiles) return;
-  Place now = place(tile);
-  rows_of(now.tok);
-  load(s0);
-  const LaneTurns turns = lane_turns(p, plan, lane);
-  int64_t ahead[2];  // positions of the warp's (quad: next) token
+  const uint32_t up = p.floor_mode ? 0u : kE4m3Up;
+  if (rd_tile >= p.tiles) return;
+  rd_start(place(rd_tile).tok);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) ahead[i] = p.quad ? rope_position(p, now.tok * p.pos_tok + turns.axis[i]) : 0;
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  const LaneTurns turns = lane_turns(p, plan, lane);
+  uint32_t stage = 0;
+  auto take = [&](RawRow<TIn> (&raw)[kBatch]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) raw[u].load_shared(ring + stage + u * (kStageBytes / kBatch), lane);
+    stage = stage + kStageBytes == kStages * kStageBytes ? 0 : stage + kStageBytes;
+  };
 
 #pragma unroll 1
-  for (; tile < p.tiles; tile += gridDim.x) {
+  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const Place now = place(tile);
     // The angles of the warp's tokens.
     __syncwarp();  // the previous ones have been read
 #pragma unroll 1
     for (int of = 0; of < (p.quad ? 1 : 4); ++of) {
       const int64_t at = __shfl_sync(0xFFFFFFFFu, now.tok, of * 8);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t n = p.quad ? ahead[i] : rope_position(p, at * p.pos_tok + turns.axis[i]);
-        cs[(p.quad ? warp : warp * 4) + of][lane + 32 * i] = rope_turn(n, turns.f[i]);
-      }
+      for (int i = 0; i < 2; ++i)
+        cs[(p.quad ? warp : warp * 4) + of][lane + 32 * i] =
+            rope_turn(rope_position(p, at * p.pos_tok + turns.axis[i]), turns.f[i]);
     }
     __syncwarp();
-    // The next tile: its rows' first loads follow this one's last.
-    const bool more = tile + static_cast<int>(gridDim.x) < p.tiles;
-    const Place after = more ? place(tile + gridDim.x) : now;
-    if (p.quad && more) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) ahead[i] = rope_position(p, after.tok * p.pos_tok + turns.axis[i]);
-    }
 
     // The tensor that the steps have come to.
     Turn m;
-    int heads = 0, head = 0;
+    int head = 0;
     bool per_head = false;
     uint8_t *sf = nullptr, *bytes = nullptr;
     __nv_bfloat16* out16 = nullptr;
@@ -411,13 +492,12 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       const RopeTensor& t = p.t[which];
       const Pairs w = weight_pairs<kHalf>(p, t, 0, j);
       make_turn<kHalf>(m, my_cs, w, j);
-      heads = t.heads;
       per_head = t.w_head != 0;
       head = step * heads_per_step + head0;
       // Where this lane's row goes: values, or payload bytes and its scale bytes.
       if (kOut == kRopeMxfp8) {
-        sf = t.scales + (now.block * heads + head) * 512 + (now.row & 31) * 16 + (now.row >> 5) * 4;
-        bytes = static_cast<uint8_t*>(t.out) + (now.tok * heads + head) * 128 + 8 * j;
+        sf = t.scales + (now.block * t.heads + head) * 512 + (now.row & 31) * 16 + (now.row >> 5) * 4;
+        bytes = static_cast<uint8_t*>(t.out) + (now.tok * t.heads + head) * 128 + 8 * j;
       } else if (kOut == kRopeBf16) {
         out16 = static_cast<__nv_bfloat16*>(t.out) + now.tok * t.out_tok + head * t.out_head + 8 * j;
       } else {
@@ -425,94 +505,132 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       }
       out_step = heads_per_step * t.out_head;
     };
-    if (s0 < steps_q) enter(0, s0);
+    if (b0 < batches_q) enter(0, b0 * kBatch); else enter(1, (b0 - batches_q) * kBatch);
+    // One batch. The steps of a batch have nothing between them, so that their chains of shuffles
+    // and conversions overlap; a step that does not exist is computed and not stored.
 #pragma unroll 1
-    for (int st = s0; st < s1; st += kBatch) {
+    for (int b = b0; b < b1; ++b) {
+      cp_async_wait<kStages - 2>();
+      if (sizeof(TIn) == 4) __syncwarp();  // (BF16: every lane reads what it copied itself)
       RawRow<TIn> raw[kBatch];
+      take(raw);
+      issue();  // into the stage that the previous batch was taken from
+      const bool is_k = b >= batches_q;
+      if (b == batches_q && b != b0) enter(1, 0);
+      const int left = steps_of[is_k] - (is_k ? b - batches_q : b) * kBatch;
+      float x[kBatch][8], y[kBatch][8];
+      Pairs v[kBatch];
+      F2 r[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
-      if (st + kBatch < s1) {
-        load(st + kBatch);
-      } else if (more) {
-        rows_of(after.tok);
-        load(s0);
+      for (int u = 0; u < kBatch; ++u) {
+        raw[u].get(0, x[u]);
+        raw[u].get(1, y[u]);
+        v[u] = to_pairs<kHalf>(x[u], y[u]);
+        r[u] = f2(1.f, 1.f);
+      }
+      if (p.norm) {
+        float sum[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          F2 ss = f2_mul(v[u].a[0], v[u].a[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) ss = f2_fma(v[u].a[i], v[u].a[i], ss);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = f2_fma(v[u].b[i], v[u].b[i], ss);
+          sum[u] = f2_sum(ss);
+        }
+#pragma unroll
+        for (int k = 4; k; k >>= 1)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) sum[u] += __shfl_xor_sync(0xFFFFFFFFu, sum[u], k);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float inv = rsqrt_newton(sum[u] * (1.f / 128.f) + p.eps);
+          r[u] = f2(inv, inv);
+        }
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        if (st + u >= s1) break;  // the same for the whole warp
-        if (st + u == steps_q || heads == 0) enter(1, st + u - steps_q);
-        const bool real = now.real && head < heads;
         if (per_head) {
-          const Pairs w = weight_pairs<kHalf>(p, p.t[st + u >= steps_q], min(head, heads - 1), j);
+          const Pairs w = weight_pairs<kHalf>(p, p.t[is_k], u < left ? head + u * heads_per_step : head, j);
           make_turn<kHalf>(m, my_cs, w, j);
-        }
-        float x[8], y[8];
-        raw[u].get(0, x);
-        raw[u].get(1, y);
-        Pairs v = to_pairs<kHalf>(x, y);
-        F2 r = f2(1.f, 1.f);
-        if (p.norm) {
-          F2 ss = f2_mul(v.a[0], v.a[0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) ss = f2_fma(v.a[i], v.a[i], ss);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ss = f2_fma(v.b[i], v.b[i], ss);
-          const float inv = rsqrt_newton(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
-          r = f2(inv, inv);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const F2 a = f2_mul(v.a[i], r), b = f2_mul(v.b[i], r);
-          v.a[i] = f2_fma(a, m.ac[i], f2_mul(b, m.bs[i]));
-          v.b[i] = f2_fma(a, m.as[i], f2_mul(b, m.bc[i]));
+          const F2 a = f2_mul(v[u].a[i], r[u]), b = f2_mul(v[u].b[i], r[u]);
+          v[u].a[i] = f2_fma(a, m.ac[i], f2_mul(b, m.bs[i]));
+          v[u].b[i] = f2_fma(a, m.as[i], f2_mul(b, m.bc[i]));
         }
-        from_pairs<kHalf>(v, x, y);
-        if (kOut == kRopeMxfp8) {
-          // The quantizer's rule (quantize.cuh): a 32-element block is a chunk of four lanes.
-          uint32_t sfw = 0;
+        from_pairs<kHalf>(v[u], x[u], y[u]);
+      }
+      if (kOut == kRopeMxfp8) {
+        // The quantizer's rule (quantize.cuh): a 32-element block is a chunk of four lanes.
+        float amax[kBatch][2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float(&z)[8] = k ? y : x;
-            float amax = chunk_amax(z);
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const int e = e8m0_exponent(amax, p.floor_mode);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const F2 inv2 = f2(inv, inv);
-            uint32_t c[4];
+        for (int u = 0; u < kBatch; ++u) {
+          amax[u][0] = chunk_amax(x[u]);
+          amax[u][1] = chunk_amax(y[u]);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const F2 q = f2_mul(f2(z[2 * i], z[2 * i + 1]), inv2);
-              c[i] = cvt_e4m3x2(q.x, q.y);
-            }
-            if (real)
-              *reinterpret_cast<uint2*>(bytes + 64 * k) =
-                  make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
-            sfw |= static_cast<uint32_t>(e + 127) << (16 * k);
+        for (int k = 1; k < 4; k <<= 1)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) amax[u][c] = fmaxf(amax[u][c], __shfl_xor_sync(0xFFFFFFFFu, amax[u][c], k));
+        uint32_t sfw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const uint32_t lo = e4m3_scale_byte(amax[u][0], up), hi = e4m3_scale_byte(amax[u][1], up);
+          sfw[u] = lo | (hi << 16);
+        }
+        // Blocks 0, 2 are lanes 0 .. 3's, 1, 3 lanes 4 .. 7's.
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const uint32_t mine = sfw[u];
+          sfw[u] |= __shfl_xor_sync(0xFFFFFFFFu, mine, 4) << 8;
+          if (j == 0 && u < left) *reinterpret_cast<uint32_t*>(sf) = now.real ? sfw[u] : 0x7F7F7F7Fu;
+          // Scaled as pairs, which is how they stand in the registers: chunk 0 is a and b of pairs 0 .. 3 of
+          // the lane, or every a.
+          const float inv0 = __uint_as_float((254u - (mine & 0xFFu)) << 23);  // 2^-e, normal
+          const float inv1 = __uint_as_float((254u - (mine >> 16)) << 23);
+          const F2 i0 = f2(inv0, inv0), i1 = f2(inv1, inv1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[u].a[i] = f2_mul(v[u].a[i], kHalf || i < 2 ? i0 : i1);
+            v[u].b[i] = f2_mul(v[u].b[i], !kHalf && i < 2 ? i0 : i1);
           }
-          // Blocks 0, 2 are lanes 0 .. 3's, 1, 3 lanes 4 .. 7's.
-          sfw |= __shfl_xor_sync(0xFFFFFFFFu, sfw, 4) << 8;
-          if (j == 0 && head < heads) *reinterpret_cast<uint32_t*>(sf) = now.real ? sfw : 0x7F7F7F7Fu;
+          from_pairs<kHalf>(v[u], x[u], y[u]);
+          if (now.real && u < left) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float(&z)[8] = c ? y[u] : x[u];
+              *reinterpret_cast<uint2*>(bytes + 64 * c) = make_uint2(cvt_e4m3x4(z[0], z[1], z[2], z[3]),
+                                                                     cvt_e4m3x4(z[4], z[5], z[6], z[7]));
+            }
+          }
           sf += heads_per_step * 512;
           bytes += heads_per_step * 128;
-        } else if (kOut == kRopeBf16) {
-          if (real) {
-            chunk_store(out16, x);
-            chunk_store(out16 + 64, y);
-          }
-          out16 += out_step;
-        } else {
-          if (real) {
-            chunk_store(out32, x);
-            chunk_store(out32 + 64, y);
-          }
-          out32 += out_step;
         }
-        head += heads_per_step;
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (now.real && u < left) {
+            if (kOut == kRopeBf16) {
+              chunk_store(out16, x[u]);
+              chunk_store(out16 + 64, y[u]);
+            } else {
+              chunk_store(out32, x[u]);
+              chunk_store(out32 + 64, y[u]);
+            }
+          }
+          out16 += kOut == kRopeBf16 ? out_step : 0;
+          out32 += kOut == kRopeF32 ? out_step : 0;
+        }
       }
+      head += kBatch * heads_per_step;
     }
-    now = after;
   }
+  cp_async_wait<0>();
 }
 
 // Backward. Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, each warp its own
@@ -558,7 +676,7 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
   for (int which = 0; which < 2; ++which) {
     const RopeTensor& t = p.t[which];
     if (t.heads == 0) continue;
-    const int steps = (t.heads + heads_per_step - 1) / heads_per_step;
+    const int steps = t.heads / heads_per_step;  // (quad: multiples of four)
     F2 acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
@@ -575,9 +693,8 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
         // Token s of the tile; what does not exist reads the last one there is and counts for nothing.
         auto load = [&](int s, int head) {
           const int64_t at = tok0 + min(s, ntok - 1);
-          const int h = min(head, t.heads - 1);
-          nx.load(static_cast<const T*>(t.x) + at * t.tok_stride + h * t.head_stride + 8 * j);
-          ng.load(static_cast<const T*>(t.dy) + at * t.dy_tok + h * t.dy_head + 8 * j);
+          nx.load(static_cast<const T*>(t.x) + at * t.tok_stride + head * t.head_stride + 8 * j);
+          ng.load(static_cast<const T*>(t.dy) + at * t.dy_tok + head * t.dy_head + 8 * j);
         };
         int step = kPerHead ? outer : 0;
         int s = tok_first + (p.quad ? 0 : grp);
@@ -591,14 +708,14 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           __syncthreads();
         }
         if (kPerHead && t.w_head != 0)
-          w = weight_pairs<kHalf>(p, t, min(step * heads_per_step + head0, t.heads - 1), j);
+          w = weight_pairs<kHalf>(p, t, step * heads_per_step + head0, j);
         F2 c[4], sn[4];
         if (!kPerHead && items > 0) turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
 #pragma unroll 1
         for (int it = 0; it < items; ++it) {
           const int head = step * heads_per_step + head0;
           const int now = s;
-          const bool on = now < ntok && head < t.heads;
+          const bool on = now < ntok;
           const RawRow<T> rx = nx, rg = ng;
           if (kPerHead) turn_pairs<kHalf>(cs[min(now, ntok - 1)], j, c, sn);
           // Next item.
@@ -666,7 +783,6 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           __syncthreads();
           for (int i = threadIdx.x; i < heads_per_step * 128; i += kRopeThreads) {
             const int head = outer * heads_per_step + (i >> 7);
-            if (head >= t.heads) continue;
             float sum = 0.f;
             if (p.quad) {
 #pragma unroll
