@@ -1005,8 +1005,11 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
   auto kernel = dt == LPFA_IN_FP32 ? rope_bwd_kernel<float>(half, per_head)
                                    : rope_bwd_kernel<__nv_bfloat16>(half, per_head);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  kernel<<<blocks, lpfa::kRopeThreads, 0, s>>>(p, plan);
-  cudaError_t e = cudaGetLastError();
+  const int smem = dt == LPFA_IN_FP32 ? lpfa::rope_bwd_smem<float>() : lpfa::rope_bwd_smem<__nv_bfloat16>();
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  kernel<<<blocks, lpfa::kRopeThreads, static_cast<size_t>(smem), s>>>(p, plan);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "norm and rotation backward launch");
   if (rows) {
     lpfa::qk_norm_rope_dw_kernel<<<dim3(rows, 4), 1024, 0, s>>>(p.partials, blocks, rows, p.w_rows[0], dq_weight, dk_weight);

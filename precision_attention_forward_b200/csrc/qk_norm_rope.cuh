@@ -190,6 +190,19 @@ template <> struct RawRow<float> {
   }
 };
 
+// Copies four rows of a warp (lane: its row's element 8 j, FP32: 4 j) to shared memory, for load_shared:
+// whole 128-byte runs of a row, and for FP32 with the pieces of odd runs exchanged, so that
+// load_shared's reads are free of bank conflicts.
+__device__ __forceinline__ void row_async(uint32_t dst, const __nv_bfloat16* p, int lane) {
+  cp_async16(dst + lane * 16, p, 16);
+  cp_async16(dst + 512 + lane * 16, p + 64, 16);
+}
+__device__ __forceinline__ void row_async(uint32_t dst, const float* p, int lane) {
+  const int j = lane & 7;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) cp_async16(dst + (lane >> 3) * 512 + (c * 8 + (j ^ (c & 1))) * 16, p + 32 * c, 16);
+}
+
 // The same 16 elements as eight pairs: a[i] holds the first elements of pairs 2 i and 2 i + 1, b[i]
 // the second ones. Pairs: interleaved 4 j .. 4 j + 3 and 32 + 4 j .. 32 + 4 j + 3; half 8 j .. 8 j + 7.
 struct Pairs {
@@ -430,14 +443,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       for (int u = 0; u < kBatch; ++u) {
         if (u < rd_left) {
           const uint32_t dst = ring + rd_stage + u * (kStageBytes / kBatch);
-          if (sizeof(TIn) == 2) {
-            cp_async16(dst + lane * 16, rd, 16);
-            cp_async16(dst + 512 + lane * 16, rd + 64, 16);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)  // 128 contiguous bytes of a row each: 16-byte piece 8 c + j
-              cp_async16(dst + grp * 512 + (c * 8 + (j ^ (c & 1))) * 16, rd + 32 * c, 16);
-          }
+          row_async(dst, rd, lane);
           rd += rd_step;
         }
       }
@@ -633,29 +639,37 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   cp_async_wait<0>();
 }
 
-// Backward. Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, each warp its own
-// tokens and for each all heads (steps of four rows as in the forward pass, the next one's loads
-// under way while one is computed). With one weight row for all heads a lane's sums for its 16
-// channels stay in registers to the end. With a row per head a warp keeps a step's heads while it
-// walks the tokens, and the warps' sums go through shared memory to the block's own row of partials.
-// No atomics: the same sums in the same order every time.
+// Backward. Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step
+// (four rows, as in the forward pass) that go round the warps, each with the next one on the way in its
+// shared-memory ring. With one weight row for all heads a lane's sums for its 16 channels stay in
+// registers to the end. With a row per head the block takes one step of heads at a time, and the
+// warps' sums go through shared memory to the block's own row of partials. No atomics: the same sums in
+// the same order every time.
+template <typename T> constexpr int rope_bwd_stage() { return 2 * 4 * 128 * static_cast<int>(sizeof(T)); }
+template <typename T> constexpr int rope_bwd_smem() {
+  return kRopeBwdTile * 128 * 4 + 4 * kRopeWarps * 128 * 4 + kRopeWarps * 2 * rope_bwd_stage<T>();
+}
+
 template <typename T, bool kHalf, bool kPerHead>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
-  __shared__ __align__(16) float2 cs[kRopeBwdTile][64];
-  __shared__ __align__(16) float sums[4 * kRopeWarps][128];
+  constexpr int kStage = rope_bwd_stage<T>();
+  constexpr int kLaneElems = sizeof(T) == 2 ? 8 : 4;  // elements of a copy
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);                               // [kRopeBwdTile]
+  float(*sums)[128] = reinterpret_cast<float(*)[128]>(rope_smem + kRopeBwdTile * 128 * 4);  // [4 * kRopeWarps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
+  const uint32_t ring = smem_u32(sums + 4 * kRopeWarps) + warp * 2 * kStage;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int64_t last = min(first + p.tile, p.tokens);
   const int part_rows = p.w_rows[0] + p.w_rows[1];
   float* part = p.partials + static_cast<int64_t>(blockIdx.x) * part_rows * 128;
   const int heads_per_step = p.quad ? 4 : 1;
   const int head0 = p.quad ? grp : 0;
-  const int tok_step = p.quad ? kRopeWarps : 4 * kRopeWarps;
-  const int tok_first = p.quad ? warp : warp * 4;  // of the warp; the lane's own: + (quad ? 0 : grp)
+  const int per_place = p.quad ? 1 : 4;
+  const int in_place = p.quad ? 0 : grp;
   const F2 minus = f2(-1.f, -1.f);
-
   const LaneTurns turns = lane_turns(p, plan, lane);
 
   // One weight row: the warps' sums join here. (Rows and channels of `sums` as the lanes hold them.)
@@ -683,22 +697,42 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
     Pairs w = weight_pairs<kHalf>(p, t, 0, j);
     for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
       const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
+      const int places = (ntok + per_place - 1) / per_place;
       if (last - first > kRopeBwdTile) __syncthreads();  // the angles of the previous tokens have been read
-      // Items of a warp: (token, step) pairs, steps fastest (per head: tokens fastest).
-      const int mine = tok_first < ntok ? (ntok - tok_first + tok_step - 1) / tok_step : 0;
 #pragma unroll 1
       for (int outer = 0; outer < (kPerHead ? steps : 1); ++outer) {
-        const int items = kPerHead ? mine : mine * steps;
-        RawRow<T> nx, ng;
-        // Token s of the tile; what does not exist reads the last one there is and counts for nothing.
-        auto load = [&](int s, int head) {
-          const int64_t at = tok0 + min(s, ntok - 1);
-          nx.load(static_cast<const T*>(t.x) + at * t.tok_stride + head * t.head_stride + 8 * j);
-          ng.load(static_cast<const T*>(t.dy) + at * t.dy_tok + head * t.dy_head + 8 * j);
+        // This warp's items: (place, step) number warp, warp + 8, ..., steps fastest; or (per head) the
+        // places warp, warp + 8, ... of one step.
+        const int all = kPerHead ? places : places * steps;
+        // An item's rows of x and dy into a stage; a token that does not exist reads the last one there is
+        // and counts for nothing.
+        auto issue = [&](int place, int step, int stage) {
+          const int64_t at = tok0 + min(place * per_place + in_place, ntok - 1);
+          const int head = step * heads_per_step + head0;
+          const T* x = static_cast<const T*>(t.x) + at * t.tok_stride + head * t.head_stride + kLaneElems * j;
+          const T* dy = static_cast<const T*>(t.dy) + at * t.dy_tok + head * t.dy_head + kLaneElems * j;
+          row_async(ring + stage * kStage, x, lane);
+          row_async(ring + stage * kStage + kStage / 2, dy, lane);
         };
-        int step = kPerHead ? outer : 0;
-        int s = tok_first + (p.quad ? 0 : grp);
-        if (items > 0) load(s, step * heads_per_step + head0);
+        // The item after (place, step).
+        auto advance = [&](int& place, int& step) {
+          if (kPerHead) {
+            place += kRopeWarps;
+          } else {
+            step += kRopeWarps;
+            while (step >= steps) {
+              step -= steps;
+              ++place;
+            }
+          }
+        };
+        int place = kPerHead ? warp : 0, step = kPerHead ? outer : warp;
+        if (!kPerHead) {
+          step -= kRopeWarps;
+          advance(place, step);
+        }
+        if (warp < all) issue(place, step, 0);
+        cp_async_commit();
         if (outer == 0 && (which == 0 || last - first > kRopeBwdTile)) {  // else Q's angles are still there
           for (int s = warp; s < ntok; s += kRopeWarps) {
 #pragma unroll
@@ -707,28 +741,22 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           }
           __syncthreads();
         }
-        if (kPerHead && t.w_head != 0)
-          w = weight_pairs<kHalf>(p, t, step * heads_per_step + head0, j);
-        F2 c[4], sn[4];
-        if (!kPerHead && items > 0) turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
+        if (kPerHead && t.w_head != 0) w = weight_pairs<kHalf>(p, t, outer * heads_per_step + head0, j);
+        int stage = 0;
 #pragma unroll 1
-        for (int it = 0; it < items; ++it) {
+        for (int it = warp; it < all; it += kRopeWarps, stage ^= 1) {
+          const int s = place * per_place + in_place;
           const int head = step * heads_per_step + head0;
-          const int now = s;
-          const bool on = now < ntok;
-          const RawRow<T> rx = nx, rg = ng;
-          if (kPerHead) turn_pairs<kHalf>(cs[min(now, ntok - 1)], j, c, sn);
-          // Next item.
-          bool new_token = true;
-          if (kPerHead) {
-            s += tok_step;
-          } else if (++step == steps) {
-            step = 0;
-            s += tok_step;
-          } else {
-            new_token = false;
-          }
-          if (it + 1 < items) load(s, step * heads_per_step + head0);
+          const bool on = s < ntok;
+          if (sizeof(T) == 4) __syncwarp();  // the stage to fill has been read (FP32: by other lanes too)
+          advance(place, step);
+          if (it + kRopeWarps < all) issue(place, step, stage ^ 1);
+          cp_async_commit();
+          cp_async_wait<1>();
+          if (sizeof(T) == 4) __syncwarp();
+          RawRow<T> rx, rg;
+          rx.load_shared(ring + stage * kStage, lane);
+          rg.load_shared(ring + stage * kStage + kStage / 2, lane);
 
           float u[8], v[8];
           rg.get(0, u);
@@ -739,6 +767,8 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           const Pairs x = to_pairs<kHalf>(u, v);
           F2 ss = f2(0.f, 0.f), hx = f2(0.f, 0.f);
           F2 gx[8];
+          F2 c[4], sn[4];
+          turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // Back by the angle: g_a = dy_a c + dy_b s, g_b = dy_b c - dy_a s.
@@ -770,12 +800,13 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
           }
           if (on) {
             from_pairs<kHalf>(d, u, v);
-            T* dst = static_cast<T*>(t.out) + (tok0 + now) * t.out_tok + head * t.out_head + 8 * j;
+            T* dst = static_cast<T*>(t.out) + (tok0 + s) * t.out_tok + head * t.out_head + 8 * j;
             chunk_store(dst, u);
             chunk_store(dst + 64, v);
           }
-          if (!kPerHead && new_token && it + 1 < items) turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
         }
+        cp_async_wait<0>();
+        __syncwarp();
         if (kPerHead && p.w_rows[which] > 1) {
           put_sums(acc);
 #pragma unroll
