@@ -24,11 +24,13 @@
 // both keep 11 bits over 2^-22 of the largest and vanish only below 2^-29, and the product stays
 // under 2^15. S, the softmax statistics and O are FP32.
 //
-// Split. A block has four warps, each walking its own tiles of 32 keys with its own running maximum
-// and accumulators (no barrier in the loop); cp.async keeps kAttn4Stages tiles per warp on the way.
-// The blocks of a cluster share the keys of one (sequence, key head, query tile) and join their
-// partial results through distributed shared memory: one launch, no workspace, and always the same
-// order of sums.
+// Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and
+// accumulators (no barrier in the loop); one lane fetches the tiles ahead by bulk copies, two to six
+// for a tile (a page holds 16 tokens or more), into the warp's ring. What the lanes of a row or column
+// share, they compute once: lane i turns key i's scale bytes into factors and leaves them in shared
+// memory. The blocks of a cluster share the keys of one (sequence, key head, query tile) and join
+// their partial results through distributed shared memory: one launch, no workspace, and always the
+// same order of sums.
 #pragma once
 
 #include <cstdint>
@@ -41,12 +43,23 @@
 
 namespace lpfa {
 
-constexpr int kAttn4Warps = 4;
+#ifndef LPFA_ATTN4_WARPS
+#define LPFA_ATTN4_WARPS 4
+#endif
+#ifndef LPFA_ATTN4_STAGES
+#define LPFA_ATTN4_STAGES 3
+#endif
+constexpr int kAttn4Warps = LPFA_ATTN4_WARPS;
 constexpr int kAttn4Threads = 32 * kAttn4Warps;
-constexpr int kAttn4Keys = 32;    // keys of a warp's tile
-constexpr int kAttn4Stages = 4;   // tiles per warp in shared memory
-constexpr int kAttn4StageBytes = kAttn4Keys * (64 + 64 + 4 + 4);
-constexpr int kAttn4Ring = kAttn4Stages * kAttn4StageBytes;
+constexpr int kAttn4Keys = 32;                 // keys of a warp's tile
+constexpr int kAttn4Stages = LPFA_ATTN4_STAGES;  // tiles per warp in shared memory
+constexpr int kAttn4StageBytes = kAttn4Keys * (64 + 64 + 4 + 4);  // K, V, their scale words
+// A warp's shared memory: the ring, the factors of K (4 floats a key) and of V (4 halves a key), and the
+// ring's barriers.
+constexpr int kAttn4KFactors = kAttn4Stages * kAttn4StageBytes;
+constexpr int kAttn4VFactors = kAttn4KFactors + kAttn4Keys * 16;
+constexpr int kAttn4Bars = kAttn4VFactors + kAttn4Keys * 8;
+constexpr int kAttn4Ring = kAttn4Bars + 16 * ((kAttn4Stages + 1) / 2);
 constexpr int kAttn4MaxSplit = 8;
 constexpr float kAttn4PBias = 8.f;  // P is 2^8 e^(s - m)
 constexpr int kAttn4VBias = 7;      // V's scale is 2^(7 + byte - largest byte)
@@ -119,10 +132,11 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
   return max(w & 0xFFu, (w >> 8) & 0xFFu);
 }
 
-// Physical key of row m (0..7) of an 8-row half of a fragment: 0 5 1 4 2 7 3 6. With it the eight
-// rows that a quarter warp reads for K, and the four that a half warp reads for V, fall into
-// different banks (V's 16-byte chunks are exchanged in rows 2, 3, 6, 7 as well).
+// Physical key of row m (0..7) of an 8-row half of a fragment: 0 5 1 4 2 7 3 6. With it the eight rows
+// that a quarter warp reads for K fall into different banks, and V's reads take two passes for four.
 __device__ __forceinline__ int attn4_key(int m) { return (m & 1) ? 4 + ((m >> 1) ^ 1) : m >> 1; }
+// And back: the row of the fragment that holds key k (0..7).
+__device__ __forceinline__ int attn4_row(int k) { return k < 4 ? 2 * k : 2 * ((k - 4) ^ 1) + 1; }
 
 // kTiles: tiles of 8 query rows that a block holds (rows = query tokens x query heads of a key head).
 template <int kTiles>
@@ -231,80 +245,121 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   uint32_t vref = 0;  // the largest V scale byte so far, in the four bytes of a word
 
   uint8_t* ring = smem4 + warp * kAttn4Ring;
-  const uint32_t ring_u = smem_u32(ring);
-  // Table entries of the two 16-key halves of a tile (pages hold 16 tokens or more); -1 beyond hi.
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAttn4Bars);
+  if (lane == 0) {
+    for (int i = 0; i < kAttn4Stages; ++i) mbar_init(&bars[i], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  // Table entries of the two 16-key halves of a tile; -1 beyond hi.
   const int32_t* table = p.c.table + seq * p.c.table_stride;
   auto entries = [&](int tile) {
     const int key = tile * kAttn4Keys;
     return make_int2(key < hi ? __ldg(table + (key >> p.c.page_shift)) : -1,
                      key + 16 < hi ? __ldg(table + ((key + 16) >> p.c.page_shift)) : -1);
   };
-  // Tile `tile`, whose entries are `pg`, into ring stage `st`; keys at or beyond hi become zeros.
-  // Returns the halves whose page is not in the pool (bits 0 and 1): their keys are not seen.
+  // Tile `tile`, whose entries are `pg`, into ring stage `st`: whole halves, of pages that are in the pool.
+  // Returns the halves (bits 0 and 1) that have keys but no such page: those keys are not seen.
+  const uint32_t leader = lane == 0;
   auto load_tile = [&](int tile, int2 pg, int st) {
-    const uint32_t dst = ring_u + st * kAttn4StageBytes;
+    uint8_t* dst = ring + st * kAttn4StageBytes;
     const int key0 = tile * kAttn4Keys;
-    int64_t rows_at[2];
-    uint32_t missing = 0;
+    const bool has0 = static_cast<uint32_t>(pg.x) < static_cast<uint32_t>(p.c.pages);
+    const bool has1 = static_cast<uint32_t>(pg.y) < static_cast<uint32_t>(p.c.pages);
+    const int64_t row0 = ((static_cast<int64_t>(pg.x) * p.c.heads + kvh) << p.c.page_shift) + (key0 & (p.c.page_size - 1));
+    const int64_t row1 =
+        ((static_cast<int64_t>(pg.y) * p.c.heads + kvh) << p.c.page_shift) + ((key0 + 16) & (p.c.page_size - 1));
+    fence_proxy_async_smem();  // the lanes' reads of the stage precede its next copies
+    if (has0 && has1 && row1 == row0 + 16) {
+      mbar_arrive_expect_tx(&bars[st], kAttn4StageBytes, leader);
+      bulk_load(dst, p.c.payload[0] + row0 * 64, 2048, &bars[st], leader);
+      bulk_load(dst + 2048, p.c.payload[1] + row0 * 64, 2048, &bars[st], leader);
+      bulk_load(dst + 4096, p.c.scales[0] + row0 * 4, 128, &bars[st], leader);
+      bulk_load(dst + 4224, p.c.scales[1] + row0 * 4, 128, &bars[st], leader);
+      return 0u;
+    }
+    mbar_arrive_expect_tx(&bars[st], (kAttn4StageBytes / 2) * (has0 + has1), leader);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int key = key0 + 16 * h;
-      const int page = h ? pg.y : pg.x;
-      rows_at[h] = -1;
-      if (key < hi) {
-        if (page >= 0 && page < p.c.pages) {
-          rows_at[h] = (((static_cast<int64_t>(page) * p.c.heads + kvh) << p.c.page_shift)) + (key & (p.c.page_size - 1));
-        } else {
-          missing |= 1u << h;
-          if (lane == 0) kv4_bad_entry(kKv4AttnPageSite);
-        }
-      }
+      if (!(h ? has1 : has0)) continue;
+      const int64_t row = h ? row1 : row0;
+      bulk_load(dst + 1024 * h, p.c.payload[0] + row * 64, 1024, &bars[st], leader);
+      bulk_load(dst + 2048 + 1024 * h, p.c.payload[1] + row * 64, 1024, &bars[st], leader);
+      bulk_load(dst + 4096 + 64 * h, p.c.scales[0] + row * 4, 64, &bars[st], leader);
+      bulk_load(dst + 4224 + 64 * h, p.c.scales[1] + row * 4, 64, &bars[st], leader);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 8 * j + (lane >> 2), ch = lane & 3;  // row of the tile, 16-byte chunk
-      const int64_t base = rows_at[j >> 1];
-      const bool on = base >= 0 && key0 + r < hi;
-      const int64_t off = on ? (base + (r & 15)) * 64 + ch * 16 : 0;
-      const uint32_t n = on ? 16u : 0u;
-      cp_async16(dst + r * 64 + ch * 16, p.c.payload[0] + off, n);
-      cp_async16(dst + 2048 + r * 64 + (ch ^ (r & 2)) * 16, p.c.payload[1] + off, n);
-    }
-    if (lane < 16) {
-      const int r = (lane & 7) * 4;  // four keys' scale words
-      const int64_t base = (lane & 4) ? rows_at[1] : rows_at[0];
-      const int left = hi - key0 - r;
-      const bool on = base >= 0 && left > 0;
-      cp_async16(dst + 4096 + lane * 16, p.c.scales[lane >> 3] + (on ? (base + (r & 15)) * 4 : 0),
-                 on ? static_cast<uint32_t>(min(16, 4 * left)) : 0u);
-    }
+    const uint32_t missing = (key0 < hi && !has0 ? 1u : 0u) | (key0 + 16 < hi && !has1 ? 2u : 0u);
+    if (missing && lane == 0) kv4_bad_entry(kKv4AttnPageSite);
     return missing;
   };
 
-  const int mine = tile0 + warp;  // this warp's tiles: mine, mine + 4, ...
+  const int mine = tile0 + warp;  // this warp's tiles: mine, mine + kAttn4Warps, ...
   uint32_t bad = 0;  // two bits per stage: halves whose page is missing
 #pragma unroll
   for (int st = 0; st < kAttn4Stages - 1; ++st) {
     const int tile = mine + st * kAttn4Warps;
     if (tile < tile1) bad |= load_tile(tile, entries(tile), st) << (2 * st);
-    cp_async_commit();
+  }
+  // Where lane i leaves key i's factors, and where a lane finds those of its fragment's keys.
+  float4* kfac = reinterpret_cast<float4*>(ring + kAttn4KFactors);
+  uint8_t* vfac = ring + kAttn4VFactors;  // [tile of 16][pair t][half of 8][block] half2 (keys 2t, 2t + 1)
+  uint16_t* vfac_mine;
+  {
+    const int m = attn4_row(lane & 7);
+    vfac_mine = reinterpret_cast<uint16_t*>(vfac + (((lane >> 4) * 4 + (m >> 1)) * 2 + ((lane >> 3) & 1)) * 16) + (m & 1);
   }
   int st = 0;
+  uint32_t phase = 0;
   int2 ahead = entries(mine + (kAttn4Stages - 1) * kAttn4Warps);  // loaded a tile before they are needed
+#pragma unroll 1
   for (int tile = mine; tile < tile1; tile += kAttn4Warps) {
-    cp_async_wait<kAttn4Stages - 2>();
-    __syncwarp();  // every lane's copies of this tile have landed, and the stage to refill was read
+    __syncwarp();  // the stage to refill, and the factors, have been read
     const int next = tile + (kAttn4Stages - 1) * kAttn4Warps;
-    const int nst = (st + kAttn4Stages - 1) % kAttn4Stages;
+    const int nst = st == 0 ? kAttn4Stages - 1 : st - 1;
     bad &= ~(3u << (2 * nst));
     if (next < tile1) bad |= load_tile(next, ahead, nst) << (2 * nst);
     ahead = entries(next + kAttn4Warps);
-    cp_async_commit();
+    if (!mbar_wait(&bars[st], phase, nullptr)) {
+      if (atomicCAS(&g_lpfa_status[0], 0, 4 /* LPFA_ERR_TIMEOUT */) == 0) atomicExch(&g_lpfa_status[1], kKv4AttnWaitSite);
+      break;
+    }
 
     const uint8_t* kt = ring + st * kAttn4StageBytes;
     const uint8_t* vt = kt + 2048;
-    const uint32_t* ksf = reinterpret_cast<const uint32_t*>(kt + 4096);
-    const uint32_t* vsf = ksf + kAttn4Keys;
+    const uint32_t gone = (bad >> (2 * st)) & 3u;
+    // ---- factors of key `lane`; keys beyond hi or without a page count as 0
+    {
+      const bool there = tile * kAttn4Keys + lane < hi && !((gone >> (lane >> 4)) & 1u);
+      const uint32_t kw = there ? *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane) : 0u;
+      const uint32_t vw = there ? *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane) : 0u;
+      // V's reference follows the largest byte.
+      const uint32_t larger = __vmaxu4(vw, vref);
+      if (__any_sync(0xFFFFFFFFu, larger != vref)) {
+        const uint32_t big = __reduce_max_sync(0xFFFFFFFFu, max_byte(larger));
+        const int down = static_cast<int>(vref & 0xFFu) - static_cast<int>(big);
+        vref = big * 0x01010101u;
+        const float fv = down < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + down) << 23);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][d][i] *= fv;
+      }
+      // K: 2^e as floats (byte 0, 2^-127, counts as 0).
+      kfac[lane] = make_float4(__uint_as_float((kw & 0xFFu) << 23), __uint_as_float((kw << 15) & 0x7F800000u),
+                               __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
+      // V: f16 2^(7 + byte - reference), the exponent field, 0 (value 0) where it would be below 1.
+      const uint32_t bias =
+          (0xFFFFu & static_cast<uint32_t>(15 + kAttn4VBias - static_cast<int>(vref & 0xFFu))) * 0x00010001u;
+      const uint32_t f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, bias, 0u) << 10;
+      const uint32_t f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, bias, 0u) << 10;
+      vfac_mine[0] = static_cast<uint16_t>(f02);
+      vfac_mine[2] = static_cast<uint16_t>(f13);
+      vfac_mine[4] = static_cast<uint16_t>(f02 >> 16);
+      vfac_mine[6] = static_cast<uint16_t>(f13 >> 16);
+      __syncwarp();
+    }
 
     // ---- S^T (two tiles of 16 keys): c0, c1: key attn4_key(g), c2, c3: 8 more; columns 2t, 2t + 1
     float s[2][kTiles][4];
@@ -313,7 +368,8 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       const int r0 = 16 * h + attn4_key(g);
       const uint4 k0 = *reinterpret_cast<const uint4*>(kt + r0 * 64 + t * 16);
       const uint4 k1 = *reinterpret_cast<const uint4*>(kt + (r0 + 8) * 64 + t * 16);
-      const uint32_t f0 = ksf[r0], f1 = ksf[r0 + 8];
+      const float4 f0 = kfac[r0], f1 = kfac[r0 + 8];
+      const float x0[4] = {f0.x, f0.y, f0.z, f0.w}, x1[4] = {f1.x, f1.y, f1.z, f1.w};
       // Byte 2 (b % 2) + j of word b / 2 (elements 8t .. + 3 of block b) or 2 + b / 2 (8t + 4 ..).
       const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -327,8 +383,6 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
           a[e][2] = (b & 1) ? cvt_e2m1x2_to_f16x2<3>(w0) : cvt_e2m1x2_to_f16x2<1>(w0);
           a[e][3] = (b & 1) ? cvt_e2m1x2_to_f16x2<3>(w1) : cvt_e2m1x2_to_f16x2<1>(w1);
         }
-        const float x0 = __uint_as_float(((f0 >> (8 * b)) & 0xFFu) << 23);  // byte 0 (2^-127) counts as 0
-        const float x1 = __uint_as_float(((f1 >> (8 * b)) & 0xFFu) << 23);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
           float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -336,40 +390,44 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
           for (int e = 0; e < 2; ++e)
             mma_f16(d, a[e][0], a[e][1], a[e][2], a[e][3], qf[n][b][2 * e], qf[n][b][2 * e + 1]);
           if (b == 0) {
-            s[h][n][0] = d[0] * x0;
-            s[h][n][1] = d[1] * x0;
-            s[h][n][2] = d[2] * x1;
-            s[h][n][3] = d[3] * x1;
+            s[h][n][0] = d[0] * x0[0];
+            s[h][n][1] = d[1] * x0[0];
+            s[h][n][2] = d[2] * x1[0];
+            s[h][n][3] = d[3] * x1[0];
           } else {
-            s[h][n][0] = fmaf(d[0], x0, s[h][n][0]);
-            s[h][n][1] = fmaf(d[1], x0, s[h][n][1]);
-            s[h][n][2] = fmaf(d[2], x1, s[h][n][2]);
-            s[h][n][3] = fmaf(d[3], x1, s[h][n][3]);
+            s[h][n][0] = fmaf(d[0], x0[b], s[h][n][0]);
+            s[h][n][1] = fmaf(d[1], x0[b], s[h][n][1]);
+            s[h][n][2] = fmaf(d[2], x1[b], s[h][n][2]);
+            s[h][n][3] = fmaf(d[3], x1[b], s[h][n][3]);
           }
         }
       }
     }
 
     // ---- log2 units, masks, running maximum
-    const int key0 = tile * kAttn4Keys + attn4_key(g);
-    const uint32_t gone = (bad >> (2 * st)) & 3u;
-    const bool masked = gone != 0 || (tile + 1) * kAttn4Keys > lim_min;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[h][n][i] *= c2[n][i & 1];
+    if (gone != 0 || (tile + 1) * kAttn4Keys > lim_min) {
+      const int key0 = tile * kAttn4Keys + attn4_key(g);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key0 + 16 * h + 8 * (i >> 1) >= lim[n][i & 1] || ((gone >> h) & 1u)) s[h][n][i] = -INFINITY;
+    }
     float top[kTiles][2];
     bool moved = false;
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[h][n][2 * e + i] * c2[n][i];
-            if (masked && (key0 + 16 * h + 8 * e >= lim[n][i] || ((gone >> h) & 1u))) x = -INFINITY;
-            s[h][n][2 * e + i] = x;
-            m = fmaxf(m, x);
-          }
+        float m = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -377,16 +435,7 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
         moved |= m > mx[n][i];
       }
     }
-    // ---- V scales: the reference follows the largest byte
-    const uint32_t vw = vsf[lane];
-    uint32_t big = __vmaxu4(vw, vref);
-    const bool grew = big != vref;
-    if (__any_sync(0xFFFFFFFFu, moved || grew)) {
-      big = max_byte(big);
-      big = __reduce_max_sync(0xFFFFFFFFu, big);
-      const int down = static_cast<int>(vref & 0xFFu) - static_cast<int>(big);
-      vref = big * 0x01010101u;
-      const float fv = down < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + down) << 23);
+    if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
@@ -397,8 +446,8 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
           l[n][i] *= f;
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
-            o[n][d][i] *= f * fv;
-            o[n][d][2 + i] *= f * fv;
+            o[n][d][i] *= f;
+            o[n][d][2 + i] *= f;
           }
         }
       }
@@ -421,61 +470,57 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       }
     }
     // ---- O^T += V^T P^T
-    const uint32_t bias = (0x0000FFFFu & static_cast<uint32_t>(15 + kAttn4VBias - static_cast<int>(vref & 0xFFu))) * 0x00010001u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // Physical keys of fragment keys 2t, 2t + 1, 2t + 8, 2t + 9.
-      const int ra = 16 * h + t, rb = 16 * h + 4 + (t ^ 1);
-      const int ga = ((g >> 1) ^ (ra & 2)) * 16 + (g & 1) * 8, gb = ((g >> 1) ^ (rb & 2)) * 16 + (g & 1) * 8;
-      const uint2 va = *reinterpret_cast<const uint2*>(vt + ra * 64 + ga);
-      const uint2 vb = *reinterpret_cast<const uint2*>(vt + rb * 64 + gb);
-      const uint2 vc = *reinterpret_cast<const uint2*>(vt + (ra + 8) * 64 + ga);
-      const uint2 vd = *reinterpret_cast<const uint2*>(vt + (rb + 8) * 64 + gb);
-      const uint32_t sa = vsf[ra], sb = vsf[rb], sc = vsf[ra + 8], sd = vsf[rb + 8];
+      // Physical keys of fragment keys 2t, 2t + 1 (and 2t + 8, 2t + 9: 8 more).
+      const uint8_t* ra = vt + (16 * h + t) * 64 + g * 8;
+      const uint8_t* rb = vt + (16 * h + 4 + (t ^ 1)) * 64 + g * 8;
+      const uint2 va = *reinterpret_cast<const uint2*>(ra), vb = *reinterpret_cast<const uint2*>(rb);
+      const uint2 vc = *reinterpret_cast<const uint2*>(ra + 512), vd = *reinterpret_cast<const uint2*>(rb + 512);
+      const uint4 fab = *reinterpret_cast<const uint4*>(vfac + ((h * 4 + t) * 2) * 16);
+      const uint4 fcd = *reinterpret_cast<const uint4*>(vfac + ((h * 4 + t) * 2 + 1) * 16);
+      const uint32_t sab[4] = {fab.x, fab.y, fab.z, fab.w}, scd[4] = {fcd.x, fcd.y, fcd.z, fcd.w};
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        // f16 2^(7 + byte - vref) of the key pairs: exponent field, 0 (value 0) where it would be < 1.
-        const uint32_t pick = 0x400u + 0x101u * static_cast<uint32_t>(b);  // byte b of the first, byte b of the second
-        const uint32_t fab = __viaddmax_s16x2_relu(__byte_perm(sa, sb, pick) & 0x00FF00FFu, bias, 0u) << 10;
-        const uint32_t fcd = __viaddmax_s16x2_relu(__byte_perm(sc, sd, pick) & 0x00FF00FFu, bias, 0u) << 10;
-        uint32_t p0[kTiles], p1[kTiles];
+      for (int half = 0; half < 2; ++half) {  // blocks 2 half, 2 half + 1
+        const uint32_t wa = half ? va.y : va.x, wb = half ? vb.y : vb.x;
+        const uint32_t wc = half ? vc.y : vc.x, wd = half ? vd.y : vd.x;
+        // Bytes of (first key's, second key's) codes: of the even elements, of the odd ones.
+        const uint32_t e0 = (wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u);
+        const uint32_t o0 = ((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u);
+        const uint32_t e1 = (wc & 0x0F0F0F0Fu) | ((wd << 4) & 0xF0F0F0F0u);
+        const uint32_t o1 = ((wc >> 4) & 0x0F0F0F0Fu) | (wd & 0xF0F0F0F0u);
+        uint32_t a[4][4];  // [byte][fragment register]
+        a[0][0] = cvt_e2m1x2_to_f16x2<0>(e0); a[0][1] = cvt_e2m1x2_to_f16x2<0>(o0);
+        a[0][2] = cvt_e2m1x2_to_f16x2<0>(e1); a[0][3] = cvt_e2m1x2_to_f16x2<0>(o1);
+        a[1][0] = cvt_e2m1x2_to_f16x2<1>(e0); a[1][1] = cvt_e2m1x2_to_f16x2<1>(o0);
+        a[1][2] = cvt_e2m1x2_to_f16x2<1>(e1); a[1][3] = cvt_e2m1x2_to_f16x2<1>(o1);
+        a[2][0] = cvt_e2m1x2_to_f16x2<2>(e0); a[2][1] = cvt_e2m1x2_to_f16x2<2>(o0);
+        a[2][2] = cvt_e2m1x2_to_f16x2<2>(e1); a[2][3] = cvt_e2m1x2_to_f16x2<2>(o1);
+        a[3][0] = cvt_e2m1x2_to_f16x2<3>(e0); a[3][1] = cvt_e2m1x2_to_f16x2<3>(o0);
+        a[3][2] = cvt_e2m1x2_to_f16x2<3>(e1); a[3][3] = cvt_e2m1x2_to_f16x2<3>(o1);
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          p0[n] = half2_mul(pb[h][n][0], fab);
-          p1[n] = half2_mul(pb[h][n][1], fcd);
-        }
-        const uint32_t wa = b < 2 ? va.x : va.y, wb = b < 2 ? vb.x : vb.y;
-        const uint32_t wc = b < 2 ? vc.x : vc.y, wd = b < 2 ? vd.x : vd.y;
+        for (int k = 0; k < 2; ++k) {
+          const int b = 2 * half + k;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t xa, xb, xc, xd;
-          if ((b & 1) == 0 && j == 0) {
-            xa = cvt_e2m1x2_to_f16x2<0>(wa); xb = cvt_e2m1x2_to_f16x2<0>(wb);
-            xc = cvt_e2m1x2_to_f16x2<0>(wc); xd = cvt_e2m1x2_to_f16x2<0>(wd);
-          } else if ((b & 1) == 0) {
-            xa = cvt_e2m1x2_to_f16x2<1>(wa); xb = cvt_e2m1x2_to_f16x2<1>(wb);
-            xc = cvt_e2m1x2_to_f16x2<1>(wc); xd = cvt_e2m1x2_to_f16x2<1>(wd);
-          } else if (j == 0) {
-            xa = cvt_e2m1x2_to_f16x2<2>(wa); xb = cvt_e2m1x2_to_f16x2<2>(wb);
-            xc = cvt_e2m1x2_to_f16x2<2>(wc); xd = cvt_e2m1x2_to_f16x2<2>(wd);
-          } else {
-            xa = cvt_e2m1x2_to_f16x2<3>(wa); xb = cvt_e2m1x2_to_f16x2<3>(wb);
-            xc = cvt_e2m1x2_to_f16x2<3>(wc); xd = cvt_e2m1x2_to_f16x2<3>(wd);
+          for (int n = 0; n < kTiles; ++n) {
+            const uint32_t p0 = half2_mul(pb[h][n][0], sab[b]), p1 = half2_mul(pb[h][n][1], scd[b]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              mma_f16(o[n][2 * b + j], a[2 * k + j][0], a[2 * k + j][1], a[2 * k + j][2], a[2 * k + j][3], p0, p1);
           }
-          const uint32_t a0 = __byte_perm(xa, xb, 0x5410), a1 = __byte_perm(xa, xb, 0x7632);
-          const uint32_t a2 = __byte_perm(xc, xd, 0x5410), a3 = __byte_perm(xc, xd, 0x7632);
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) mma_f16(o[n][2 * b + j], a0, a1, a2, a3, p0[n], p1[n]);
         }
       }
     }
-    st = st + 1 == kAttn4Stages ? 0 : st + 1;
+    if (++st == kAttn4Stages) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
-  cp_async_wait<0>();
   __syncwarp();
 
   // ---- join: the warp's partial (O without its bias, m, l) over its own ring, then the block's, then
-  // the cluster's.
+  // the cluster's. Rows that do not exist are left out.
+  const int real = min(kRows, rows - row0);
   float* part = reinterpret_cast<float*>(ring);  // [kRows][kPitch], then m[kRows], l[kRows]
   const int undo = static_cast<int>(vref & 0xFFu) - 127 - kAttn4VBias;
 #pragma unroll
@@ -486,6 +531,7 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
       l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
       const int row = 8 * n + 2 * t + i;
+      if (row >= real) continue;
       if (g == 0) {
         part[kRows * kPitch + row] = mx[n][i];
         part[kRows * kPitch + kRows + row] = l[n][i];
@@ -502,42 +548,27 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   constexpr int kRingFloats = kAttn4Ring / 4;
   const float* parts = reinterpret_cast<const float*>(smem4);
   float* joined = reinterpret_cast<float*>(smem4 + kAttn4Warps * kAttn4Ring);  // like a warp's partial
-  for (int row = 0; row < kRows; ++row) {
-    const int ch = threadIdx.x;
-    float m = -INFINITY, lsum = 0.f, acc = 0.f;
+  const int ch = threadIdx.x;
+  static_assert(kAttn4Threads == 128, "a thread joins one channel");
+  // Sums of the partials x < n of a row, weighted to their largest m. A partial without keys (m = -inf)
+  // has l = 0 and counts for nothing, unless its l is NaN.
+  auto join = [&](const float (&ms)[kAttn4MaxSplit], const float (&ls)[kAttn4MaxSplit],
+                  const float (&os)[kAttn4MaxSplit], int n, float& m, float& lsum, float& acc) {
+    m = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < kAttn4Warps; ++x) m = fmaxf(m, parts[x * kRingFloats + kRows * kPitch + row]);
+    for (int x = 0; x < kAttn4MaxSplit; ++x)
+      if (x < n) m = fmaxf(m, ms[x]);
+    lsum = 0.f;
+    acc = 0.f;
 #pragma unroll
-    for (int x = 0; x < kAttn4Warps; ++x) {
-      const float mw = parts[x * kRingFloats + kRows * kPitch + row];
-      const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - m);
-      const float lw = parts[x * kRingFloats + kRows * kPitch + kRows + row];
-      if (mw != -INFINITY || lw != 0.f) {  // NaN sums are kept
-        lsum += f * lw;
-        acc = fmaf(f, parts[x * kRingFloats + row * kPitch + ch], acc);
-      }
+    for (int x = 0; x < kAttn4MaxSplit; ++x) {
+      if (x >= n || (ms[x] == -INFINITY && ls[x] == 0.f)) continue;
+      const float f = ms[x] == -INFINITY ? 0.f : ex2_approx(ms[x] - m);
+      lsum = fmaf(f, ls[x], lsum);
+      acc = fmaf(f, os[x], acc);
     }
-    joined[row * kPitch + ch] = acc;
-    if (ch == 0) {
-      joined[kRows * kPitch + row] = m;
-      joined[kRows * kPitch + kRows + row] = lsum;
-    }
-  }
-  if (p.splits > 1) cluster_sync_all(); else __syncthreads();
-  const uint32_t joined_u = smem_u32(joined);
-  for (int row = static_cast<int>(split); row < kRows && row0 + row < rows; row += p.splits) {
-    const int ch = threadIdx.x;
-    float m = -INFINITY, lsum = 0.f, acc = 0.f;
-    for (int x = 0; x < p.splits; ++x) m = fmaxf(m, dsmem_ld(joined_u + (kRows * kPitch + row) * 4, x));
-    for (int x = 0; x < p.splits; ++x) {
-      const float mw = dsmem_ld(joined_u + (kRows * kPitch + row) * 4, x);
-      const float lw = dsmem_ld(joined_u + (kRows * kPitch + kRows + row) * 4, x);
-      const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - m);
-      if (mw != -INFINITY || lw != 0.f) {
-        lsum += f * lw;
-        acc = fmaf(f, dsmem_ld(joined_u + (row * kPitch + ch) * 4, x), acc);
-      }
-    }
+  };
+  auto finish = [&](int row, float m, float lsum, float acc) {
     const int rr = row0 + row;
     const int tok = rr / p.group;
     const int head = kvh * p.group + rr - tok * p.group;
@@ -546,8 +577,43 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
     if (ch == 0)  // l carries the bias 2^8 of P
       p.lse[head * p.total_q + q0 + tok] =
           lsum == 0.f ? -INFINITY : (m + lg2_approx(lsum) - kAttn4PBias) * 0.69314718055994531f;
+  };
+  for (int row = 0; row < real; ++row) {
+    float ms[kAttn4MaxSplit], ls[kAttn4MaxSplit], os[kAttn4MaxSplit], m, lsum, acc;
+#pragma unroll
+    for (int x = 0; x < kAttn4Warps; ++x) {
+      ms[x] = parts[x * kRingFloats + kRows * kPitch + row];
+      ls[x] = parts[x * kRingFloats + kRows * kPitch + kRows + row];
+      os[x] = parts[x * kRingFloats + row * kPitch + ch];
+    }
+    join(ms, ls, os, kAttn4Warps, m, lsum, acc);
+    if (p.splits == 1) {
+      finish(row, m, lsum, acc);
+    } else {
+      joined[row * kPitch + ch] = acc;
+      if (ch == 0) {
+        joined[kRows * kPitch + row] = m;
+        joined[kRows * kPitch + kRows + row] = lsum;
+      }
+    }
   }
-  if (p.splits > 1) cluster_sync_all();  // no block leaves while another reads its partial
+  if (p.splits == 1) return;
+  cluster_sync_all();
+  const uint32_t joined_u = smem_u32(joined);
+  for (int row = static_cast<int>(split); row < real; row += p.splits) {
+    // All of the remote reads on the way at once.
+    float ms[kAttn4MaxSplit], ls[kAttn4MaxSplit], os[kAttn4MaxSplit], m, lsum, acc;
+#pragma unroll
+    for (int x = 0; x < kAttn4MaxSplit; ++x) {
+      const int from = min(x, p.splits - 1);
+      ms[x] = dsmem_ld(joined_u + (kRows * kPitch + row) * 4, from);
+      ls[x] = dsmem_ld(joined_u + (kRows * kPitch + kRows + row) * 4, from);
+      os[x] = dsmem_ld(joined_u + (row * kPitch + ch) * 4, from);
+    }
+    join(ms, ls, os, p.splits, m, lsum, acc);
+    finish(row, m, lsum, acc);
+  }
+  cluster_sync_all();  // no block leaves while another reads its partial
 }
 
 template <int kTiles> constexpr uint32_t attn4_smem_bytes() {

@@ -39,7 +39,8 @@ constexpr int kKv4Tile = 32;  // tokens of a block, at most
 constexpr int kKv4Rows = kKv4Threads / 4;  // rows that a block has in hand at a time
 
 // Sites of the status word for entries out of range.
-enum Kv4Site : int { kKv4WriteSite = 300, kKv4ReadSite = 301, kKv4AttnLenSite = 302, kKv4AttnPageSite = 303 };
+enum Kv4Site : int { kKv4WriteSite = 300, kKv4ReadSite = 301, kKv4AttnLenSite = 302, kKv4AttnPageSite = 303,
+                    kKv4AttnWaitSite = 304 /* a bounded wait ran out */ };
 
 struct Kv4Cache {
   uint8_t* payload[2];  // K, V
