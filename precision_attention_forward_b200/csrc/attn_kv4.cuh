@@ -38,21 +38,17 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace lpfa {
 
-#ifndef LPFA_ATTN4_WARPS
-#define LPFA_ATTN4_WARPS 4
-#endif
-#ifndef LPFA_ATTN4_STAGES
-#define LPFA_ATTN4_STAGES 3
-#endif
-constexpr int kAttn4Warps = LPFA_ATTN4_WARPS;
-constexpr int kAttn4Threads = 32 * kAttn4Warps;
+// Warps of a block: 16 of them on an SM at 128 registers (8 query rows), 8 at twice as many (16 rows).
+template <int kTiles> constexpr int attn4_warps() { return kTiles == 1 ? 8 : 4; }
 constexpr int kAttn4Keys = 32;                 // keys of a warp's tile
-constexpr int kAttn4Stages = LPFA_ATTN4_STAGES;  // tiles per warp in shared memory
+constexpr int kAttn4Stages = 3;                // tiles per warp in shared memory
 constexpr int kAttn4StageBytes = kAttn4Keys * (64 + 64 + 4 + 4);  // K, V, their scale words
 // A warp's shared memory: the ring, the factors of K (4 floats a key) and of V (4 halves a key), and the
 // ring's barriers.
@@ -60,7 +56,8 @@ constexpr int kAttn4KFactors = kAttn4Stages * kAttn4StageBytes;
 constexpr int kAttn4VFactors = kAttn4KFactors + kAttn4Keys * 16;
 constexpr int kAttn4Bars = kAttn4VFactors + kAttn4Keys * 8;
 constexpr int kAttn4Ring = kAttn4Bars + 16 * ((kAttn4Stages + 1) / 2);
-constexpr int kAttn4MaxSplit = 8;
+constexpr int kAttn4MaxSplit = 16;  // blocks of a cluster
+constexpr int kAttn4SortMax = 512;  // sequences that are put in order
 constexpr float kAttn4PBias = 8.f;  // P is 2^8 e^(s - m)
 constexpr int kAttn4VBias = 7;      // V's scale is 2^(7 + byte - largest byte)
 
@@ -74,6 +71,7 @@ struct Attn4Params {
   int tiles;                     // query tiles of the longest sequence
   int causal;
   int splits;
+  int sorted;  // take the sequences in order of their lengths
   int64_t total_q;
   __nv_bfloat16* out;  // (Tq, heads_q, 128)
   float* lse;          // (heads_q, Tq)
@@ -90,15 +88,24 @@ __device__ __forceinline__ uint32_t cvt_e2m1x2_to_f16x2(uint32_t w) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zero.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
 
@@ -140,7 +147,10 @@ __device__ __forceinline__ int attn4_row(int k) { return k < 4 ? 2 * k : 2 * ((k
 
 // kTiles: tiles of 8 query rows that a block holds (rows = query tokens x query heads of a key head).
 template <int kTiles>
-__global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
+__global__ void __launch_bounds__(32 * attn4_warps<kTiles>(), kTiles == 1 ? 16 / attn4_warps<kTiles>() : 2)
+attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
+  constexpr int kAttn4Warps = attn4_warps<kTiles>();
+  constexpr int kAttn4Threads = 32 * kAttn4Warps;
   constexpr int kRows = 8 * kTiles;
   constexpr int kPitch = 132;  // floats per row of a partial O
   extern __shared__ __align__(16) uint8_t smem4[];
@@ -154,7 +164,24 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   const int qt = w % p.tiles;
   w /= p.tiles;
   const int kvh = w % p.c.heads;
-  const int seq = w / p.c.heads;
+  int seq = w / p.c.heads;
+  if (p.sorted) {
+    // Longest sequences first, so that the last blocks to run are short ones: sequence number `seq` of
+    // that order. Every block works it out for itself (the lengths are on the device only).
+    int32_t* lens = reinterpret_cast<int32_t*>(smem4);
+    int32_t* nth = lens + kAttn4SortMax;
+    for (int i = threadIdx.x; i < p.num_seqs; i += kAttn4Threads) lens[i] = __ldg(p.kv_lens + i);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.num_seqs; i += kAttn4Threads) {
+      const int mine = lens[i];
+      int rank = 0;
+      for (int k = 0; k < p.num_seqs; ++k) rank += lens[k] > mine || (lens[k] == mine && k < i);
+      if (rank == seq) *nth = i;
+    }
+    __syncthreads();
+    seq = *nth;
+    __syncthreads();  // the rings come next in this memory
+  }
   const int q0 = __ldg(p.cu_q + seq);
   const int lq = __ldg(p.cu_q + seq + 1) - q0;
   const int rows = lq * p.group;
@@ -253,8 +280,10 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   __syncwarp();
   // Table entries of the two 16-key halves of a tile; -1 beyond hi.
   const int32_t* table = p.c.table + seq * p.c.table_stride;
+  const bool whole = p.c.page_shift >= 5;  // a tile lies within one page
   auto entries = [&](int tile) {
     const int key = tile * kAttn4Keys;
+    if (whole) return make_int2(key < hi ? __ldg(table + (key >> p.c.page_shift)) : -1, 0);
     return make_int2(key < hi ? __ldg(table + (key >> p.c.page_shift)) : -1,
                      key + 16 < hi ? __ldg(table + ((key + 16) >> p.c.page_shift)) : -1);
   };
@@ -265,19 +294,23 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
     uint8_t* dst = ring + st * kAttn4StageBytes;
     const int key0 = tile * kAttn4Keys;
     const bool has0 = static_cast<uint32_t>(pg.x) < static_cast<uint32_t>(p.c.pages);
-    const bool has1 = static_cast<uint32_t>(pg.y) < static_cast<uint32_t>(p.c.pages);
     const int64_t row0 = ((static_cast<int64_t>(pg.x) * p.c.heads + kvh) << p.c.page_shift) + (key0 & (p.c.page_size - 1));
+    fence_proxy_async_smem();  // the lanes' reads of the stage precede its next copies
+    if (whole) {
+      mbar_arrive_expect_tx(&bars[st], has0 ? kAttn4StageBytes : 0, leader);
+      if (has0) {
+        bulk_load(dst, p.c.payload[0] + row0 * 64, 2048, &bars[st], leader);
+        bulk_load(dst + 2048, p.c.payload[1] + row0 * 64, 2048, &bars[st], leader);
+        bulk_load(dst + 4096, p.c.scales[0] + row0 * 4, 128, &bars[st], leader);
+        bulk_load(dst + 4224, p.c.scales[1] + row0 * 4, 128, &bars[st], leader);
+        return 0u;
+      }
+      if (lane == 0) kv4_bad_entry(kKv4AttnPageSite);
+      return 3u;
+    }
+    const bool has1 = static_cast<uint32_t>(pg.y) < static_cast<uint32_t>(p.c.pages);
     const int64_t row1 =
         ((static_cast<int64_t>(pg.y) * p.c.heads + kvh) << p.c.page_shift) + ((key0 + 16) & (p.c.page_size - 1));
-    fence_proxy_async_smem();  // the lanes' reads of the stage precede its next copies
-    if (has0 && has1 && row1 == row0 + 16) {
-      mbar_arrive_expect_tx(&bars[st], kAttn4StageBytes, leader);
-      bulk_load(dst, p.c.payload[0] + row0 * 64, 2048, &bars[st], leader);
-      bulk_load(dst + 2048, p.c.payload[1] + row0 * 64, 2048, &bars[st], leader);
-      bulk_load(dst + 4096, p.c.scales[0] + row0 * 4, 128, &bars[st], leader);
-      bulk_load(dst + 4224, p.c.scales[1] + row0 * 4, 128, &bars[st], leader);
-      return 0u;
-    }
     mbar_arrive_expect_tx(&bars[st], (kAttn4StageBytes / 2) * (has0 + has1), leader);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -385,10 +418,9 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
         }
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            mma_f16(d, a[e][0], a[e][1], a[e][2], a[e][3], qf[n][b][2 * e], qf[n][b][2 * e + 1]);
+          float d[4];
+          mma_f16_zero(d, a[0][0], a[0][1], a[0][2], a[0][3], qf[n][b][0], qf[n][b][1]);
+          mma_f16(d, a[1][0], a[1][1], a[1][2], a[1][3], qf[n][b][2], qf[n][b][3]);
           if (b == 0) {
             s[h][n][0] = d[0] * x0[0];
             s[h][n][1] = d[1] * x0[0];
@@ -404,13 +436,7 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       }
     }
 
-    // ---- log2 units, masks, running maximum
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[h][n][i] *= c2[n][i & 1];
+    // ---- masks, running maximum (in log2 units: the factor is positive, so it can follow the maximum)
     if (gone != 0 || (tile + 1) * kAttn4Keys > lim_min) {
       const int key0 = tile * kAttn4Keys + attn4_key(g);
 #pragma unroll
@@ -431,8 +457,8 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-        top[n][i] = m;
-        moved |= m > mx[n][i];
+        top[n][i] = m * c2[n][i];
+        moved |= top[n][i] > mx[n][i];
       }
     }
     if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -461,8 +487,8 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       const float r1 = mx[n][1] == -INFINITY ? 0.f : kAttn4PBias - mx[n][1];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float e0 = ex2_approx(s[h][n][0] + r0), e1 = ex2_approx(s[h][n][1] + r1);
-        const float e2 = ex2_approx(s[h][n][2] + r0), e3 = ex2_approx(s[h][n][3] + r1);
+        const float e0 = ex2_approx(fmaf(s[h][n][0], c2[n][0], r0)), e1 = ex2_approx(fmaf(s[h][n][1], c2[n][1], r1));
+        const float e2 = ex2_approx(fmaf(s[h][n][2], c2[n][0], r0)), e3 = ex2_approx(fmaf(s[h][n][3], c2[n][1], r1));
         l[n][0] += e0 + e2;
         l[n][1] += e1 + e3;
         pb[h][n][0] = movmatrix(half2_bits(e0, e1));
@@ -547,21 +573,24 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   __syncthreads();
   constexpr int kRingFloats = kAttn4Ring / 4;
   const float* parts = reinterpret_cast<const float*>(smem4);
-  float* joined = reinterpret_cast<float*>(smem4 + kAttn4Warps * kAttn4Ring);  // like a warp's partial
-  const int ch = threadIdx.x;
-  static_assert(kAttn4Threads == 128, "a thread joins one channel");
+  // Like a warp's partial; behind the first warp's in its ring, or (16 rows) behind all rings.
+  float* joined = reinterpret_cast<float*>(smem4) +
+                  (kTiles == 1 ? kRows * (kPitch + 2) : kAttn4Warps * kRingFloats);
+  static_assert(kAttn4Warps <= kAttn4MaxSplit && 2 * 8 * (kPitch + 2) * 4 <= kAttn4Ring, "partials fit");
+  const int ch = threadIdx.x & 127;
+  constexpr int kJoiners = kAttn4Threads / 128;  // threads that join the rows of a channel
   // Sums of the partials x < n of a row, weighted to their largest m. A partial without keys (m = -inf)
   // has l = 0 and counts for nothing, unless its l is NaN.
-  auto join = [&](const float (&ms)[kAttn4MaxSplit], const float (&ls)[kAttn4MaxSplit],
-                  const float (&os)[kAttn4MaxSplit], int n, float& m, float& lsum, float& acc) {
+  auto join = [&](const auto& ms, const auto& ls, const auto& os, int n, float& m, float& lsum, float& acc) {
+    constexpr int kMost = sizeof(ms) / sizeof(float);
     m = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < kAttn4MaxSplit; ++x)
+    for (int x = 0; x < kMost; ++x)
       if (x < n) m = fmaxf(m, ms[x]);
     lsum = 0.f;
     acc = 0.f;
 #pragma unroll
-    for (int x = 0; x < kAttn4MaxSplit; ++x) {
+    for (int x = 0; x < kMost; ++x) {
       if (x >= n || (ms[x] == -INFINITY && ls[x] == 0.f)) continue;
       const float f = ms[x] == -INFINITY ? 0.f : ex2_approx(ms[x] - m);
       lsum = fmaf(f, ls[x], lsum);
@@ -578,8 +607,8 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
       p.lse[head * p.total_q + q0 + tok] =
           lsum == 0.f ? -INFINITY : (m + lg2_approx(lsum) - kAttn4PBias) * 0.69314718055994531f;
   };
-  for (int row = 0; row < real; ++row) {
-    float ms[kAttn4MaxSplit], ls[kAttn4MaxSplit], os[kAttn4MaxSplit], m, lsum, acc;
+  for (int row = threadIdx.x >> 7; row < real; row += kJoiners) {
+    float ms[kAttn4Warps], ls[kAttn4Warps], os[kAttn4Warps], m, lsum, acc;
 #pragma unroll
     for (int x = 0; x < kAttn4Warps; ++x) {
       ms[x] = parts[x * kRingFloats + kRows * kPitch + row];
@@ -600,24 +629,34 @@ __global__ void __launch_bounds__(kAttn4Threads) attn_kv4_kernel(const __grid_co
   if (p.splits == 1) return;
   cluster_sync_all();
   const uint32_t joined_u = smem_u32(joined);
-  for (int row = static_cast<int>(split); row < real; row += p.splits) {
-    // All of the remote reads on the way at once.
-    float ms[kAttn4MaxSplit], ls[kAttn4MaxSplit], os[kAttn4MaxSplit], m, lsum, acc;
+  // All of a row's remote reads on the way at once.
+  auto join_blocks = [&](auto most) {
+    constexpr int kMost = decltype(most)::value;
+    for (int row = static_cast<int>(split) + p.splits * (threadIdx.x >> 7); row < real; row += p.splits * kJoiners) {
+      float ms[kMost], ls[kMost], os[kMost], m, lsum, acc;
 #pragma unroll
-    for (int x = 0; x < kAttn4MaxSplit; ++x) {
-      const int from = min(x, p.splits - 1);
-      ms[x] = dsmem_ld(joined_u + (kRows * kPitch + row) * 4, from);
-      ls[x] = dsmem_ld(joined_u + (kRows * kPitch + kRows + row) * 4, from);
-      os[x] = dsmem_ld(joined_u + (row * kPitch + ch) * 4, from);
+      for (int x = 0; x < kMost; ++x) {
+        const int from = min(x, p.splits - 1);
+        ms[x] = dsmem_ld(joined_u + (kRows * kPitch + row) * 4, from);
+        ls[x] = dsmem_ld(joined_u + (kRows * kPitch + kRows + row) * 4, from);
+        os[x] = dsmem_ld(joined_u + (row * kPitch + ch) * 4, from);
+      }
+      join(ms, ls, os, p.splits, m, lsum, acc);
+      finish(row, m, lsum, acc);
     }
-    join(ms, ls, os, p.splits, m, lsum, acc);
-    finish(row, m, lsum, acc);
+  };
+  if (p.splits <= 4) {
+    join_blocks(std::integral_constant<int, 4>{});
+  } else if (p.splits <= 8) {
+    join_blocks(std::integral_constant<int, 8>{});
+  } else {
+    join_blocks(std::integral_constant<int, kAttn4MaxSplit>{});
   }
   cluster_sync_all();  // no block leaves while another reads its partial
 }
 
 template <int kTiles> constexpr uint32_t attn4_smem_bytes() {
-  return kAttn4Warps * kAttn4Ring + (8 * kTiles * 132 + 16 * kTiles) * 4;
+  return attn4_warps<kTiles>() * kAttn4Ring + (kTiles == 1 ? 0 : 16 * 134 * 4);
 }
 
 }  // namespace lpfa

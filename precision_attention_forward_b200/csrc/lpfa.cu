@@ -1123,37 +1123,66 @@ lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* ta
 }
 
 extern "C++" {
+namespace {
+
+// Clusters of n blocks of the cache attention that the current device runs at a time, looked up once.
 template <int kTiles>
-static lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, cudaStream_t s) {
+int attn4_clusters(const cudaLaunchConfig_t& cfg, int dev, int n) {
+  static int known[kMaxDevices][lpfa::kAttn4MaxSplit + 1] = {};  // 0: not looked up; else count + 1
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  int& k = known[dev][n];
+  if (k == 0) {
+    int count = 0;
+    if (cudaOccupancyMaxActiveClusters(&count, lpfa::attn_kv4_kernel<kTiles>, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // a size that this device does not have
+      count = 0;
+    }
+    k = count + 1;
+  }
+  return k - 1;
+}
+
+template <int kTiles>
+lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, int dev, cudaStream_t s) {
   constexpr uint32_t smem = lpfa::attn4_smem_bytes<kTiles>();
   auto kernel = lpfa::attn_kv4_kernel<kTiles>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const int64_t tiles = (max_rows + 8 * kTiles - 1) / (8 * kTiles);
   const int64_t work = tiles * p.c.heads * p.num_seqs;
   if (work > INT32_MAX / lpfa::kAttn4MaxSplit) return fail(LPFA_ERR_INVALID_ARG, "too many query tiles");
   p.tiles = static_cast<int>(tiles);
-  // Blocks for a few waves of three per SM (ragged lengths need the slack), but a split of at least
-  // 256 keys, two tiles for each of its warps.
-  const int64_t keys = static_cast<int64_t>(p.c.width) << p.c.page_shift;
-  p.splits = 1;
-  while (p.splits < lpfa::kAttn4MaxSplit && work * p.splits < 6 * sms && keys >= 2 * 256 * static_cast<int64_t>(p.splits))
-    p.splits *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(work * p.splits));
-  cfg.blockDim = dim3(lpfa::kAttn4Threads);
+  cfg.blockDim = dim3(32 * lpfa::attn4_warps<kTiles>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // As many blocks as run at a time, two per SM, but 128 keys for each at least. (Two rounds of half
+  // as long blocks took 35 instead of 25 us for 8 x 5 query tokens over 4096 keys.) Clusters beyond
+  // the portable size of 8 only where the device can place all of them at once.
+  const int64_t keys = static_cast<int64_t>(p.c.width) << p.c.page_shift;
+  p.splits = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({lpfa::kAttn4MaxSplit, 2 * sms / work, keys / 128})));
+  for (;; --p.splits) {
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    cfg.gridDim = dim3(static_cast<unsigned>(work * p.splits));
+    if (p.splits <= 8 || attn4_clusters<kTiles>(cfg, dev, p.splits) >= work) break;
+  }
+  // Blocks that have to wait for others' places run in order of length (64 ragged sequences of up to
+  // 8192 keys: 80 instead of 106 us).
+  p.sorted = p.num_seqs > 1 && p.num_seqs <= lpfa::kAttn4SortMax && work * p.splits > 2 * sms;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache attention launch");
 }
+
+}  // namespace
 }  // extern "C++"
 
 lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_kv4_cache* cache,
@@ -1185,11 +1214,15 @@ lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_k
   const int64_t max_rows = static_cast<int64_t>(meta_q->max_seqlen) * p.group;
   if (max_rows > INT32_MAX / 2) return fail(LPFA_ERR_INVALID_ARG, "too many query rows in a sequence");
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info)) != LPFA_OK || (st = current_device(&info, &dev)) != LPFA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // One row costs what eight do: eight rows per block where that is all there are, else sixteen, which
-  // halves the reads of the cache.
-  return max_rows <= 8 ? launch_attn_kv4<1>(p, max_rows, info.sms, s) : launch_attn_kv4<2>(p, max_rows, info.sms, s);
+  // One row costs what eight do. Sixteen per block halve the conversions and the reads of the cache,
+  // with half as many warps on an SM: worth it for more than eight rows, where the largest split still
+  // fills the card (16 rows: 32 x 8192 keys 70 instead of 80 us, but 4 x 65536 keys 116 instead of 81).
+  const int64_t work16 = (max_rows + 15) / 16 * p.c.heads * p.num_seqs;
+  return max_rows <= 8 || work16 * 8 < 2 * info.sms ? launch_attn_kv4<1>(p, max_rows, info.sms, dev, s)
+                                                    : launch_attn_kv4<2>(p, max_rows, info.sms, dev, s);
 }
 
 lpfa_status lpfa_device_status(void* stream, int32_t* detail) {
