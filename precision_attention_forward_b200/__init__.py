@@ -920,14 +920,13 @@ def lpfa_kv4_read(cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta, s
     _check_meta_device(meta, device)
     table = _page_table(page_table, meta.num_seqs, device)
     starts = _seq_ints(start, "start", meta.num_seqs, device)
-    T, H = meta.total_tokens, cache.heads
-    nb = meta.total_scale_blocks * H * 512
+    shape, nb = (meta.total_tokens, cache.heads, 128), (meta.total_scale_blocks * cache.heads * 512,)
+    u8 = torch.uint8
     with _Scope(device, stream) as sc:
-        outs = []
-        for t, name, shape in ((k_payload, "k_payload", (T, H, 128)), (k_scales, "k_scales", (nb,)),
-                               (v_payload, "v_payload", (T, H, 128)), (v_scales, "v_scales", (nb,))):
-            outs.append(sc.empty(shape, torch.uint8) if t is None else _contiguous(t, name, torch.uint8, device, shape))
-        k, ks, v, vs = outs
+        k = sc.empty(shape, u8) if k_payload is None else _contiguous(k_payload, "k_payload", u8, device, shape)
+        ks = sc.empty(nb, u8) if k_scales is None else _contiguous(k_scales, "k_scales", u8, device, nb)
+        v = sc.like(k, u8) if v_payload is None else _contiguous(v_payload, "v_payload", u8, device, shape)
+        vs = sc.like(ks, u8) if v_scales is None else _contiguous(v_scales, "v_scales", u8, device, nb)
         _check(_lib.lpfa_kv4_read(cache._c, table, starts, meta._c, 128, k.data_ptr(), ks.data_ptr(), v.data_ptr(),
                                   vs.data_ptr(), sc.handle))
     return k, ks, v, vs

@@ -20,9 +20,10 @@
 // scaled per row by a power of two into FP16's range, which holds a BF16 value exactly down to
 // 2^-29 of the row's largest. O^T = V^T P^T: the fragment's channels lie in one scale block too, so
 // V's scale multiplies P (8 half2 products per 16 keys) and V's codes stay unscaled.
-// P is FP16 with the bias 2^8 and V's scale relative to the warp's largest one with the bias 2^7:
-// both keep 11 bits over 2^-22 of the largest and vanish only below 2^-29, and the product stays
-// under 2^15. S, the softmax statistics and O are FP32.
+// P is FP16 with the bias 2^4, relative to a reference that trails the maximum by at most 2^4, and V's
+// scale is relative to the warp's largest one with the bias 2^7: P keeps its 11 bits down to 2^-18 of
+// the largest and vanishes below 2^-28, V's scale is exact down to 2^-21 of the largest and vanishes
+// below that, and their product stays under 2^15. S, the softmax statistics and O are FP32.
 //
 // Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and
 // accumulators (no barrier in the loop); one lane fetches the tiles ahead by bulk copies, two to six
@@ -58,7 +59,8 @@ constexpr int kAttn4Bars = kAttn4VFactors + kAttn4Keys * 8;
 constexpr int kAttn4Ring = kAttn4Bars + 16 * ((kAttn4Stages + 1) / 2);
 constexpr int kAttn4MaxSplit = 16;  // blocks of a cluster
 constexpr int kAttn4SortMax = 512;  // sequences that are put in order
-constexpr float kAttn4PBias = 8.f;  // P is 2^8 e^(s - m)
+constexpr float kAttn4Lag = 4.f;    // binades that the running maximum may be exceeded by
+constexpr float kAttn4PBias = 4.f;  // P is 2^4 e^(s - m), at most 2^8
 constexpr int kAttn4VBias = 7;      // V's scale is 2^(7 + byte - largest byte)
 
 struct Attn4Params {
@@ -447,18 +449,16 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
           for (int i = 0; i < 4; ++i)
             if (key0 + 16 * h + 8 * (i >> 1) >= lim[n][i & 1] || ((gone >> h) & 1u)) s[h][n][i] = -INFINITY;
     }
-    float top[kTiles][2];
+    // The reference m follows the maximum only when a key is more than 2^kAttn4Lag above it: until then a
+    // lane needs to know its own keys' maximum alone, and no shuffles.
     bool moved = false;
+    float top[kTiles][2];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float m = fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-        top[n][i] = m * c2[n][i];
-        moved |= top[n][i] > mx[n][i];
+        top[n][i] = c2[n][i] * fmaxf(fmaxf(s[0][n][i], s[0][n][2 + i]), fmaxf(s[1][n][i], s[1][n][2 + i]));
+        moved |= top[n][i] > mx[n][i] + kAttn4Lag;
       }
     }
     if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -466,7 +466,10 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
       for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float m = fmaxf(mx[n][i], top[n][i]);
+          float m = fmaxf(mx[n][i], top[n][i]);
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
           const float f = mx[n][i] == -INFINITY ? 0.f : ex2_approx(mx[n][i] - m);  // no key yet: o and l are 0
           mx[n][i] = m;
           l[n][i] *= f;
@@ -478,7 +481,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
         }
       }
     }
-    // ---- P^T as the B operand: 2^8 e^(s - m), keys 2t, 2t + 1 (and 8 more) of column g
+    // ---- P^T as the B operand: 2^4 e^(s - m), keys 2t, 2t + 1 (and 8 more) of column g
     uint32_t pb[2][kTiles][2];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
@@ -603,7 +606,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     const int head = kvh * p.group + rr - tok * p.group;
     const float res = lsum == 0.f ? 0.f : acc / lsum;
     p.out[((q0 + static_cast<int64_t>(tok)) * p.heads_q + head) * 128 + ch] = __float2bfloat16(res);
-    if (ch == 0)  // l carries the bias 2^8 of P
+    if (ch == 0)  // l carries P's bias
       p.lse[head * p.total_q + q0 + tok] =
           lsum == 0.f ? -INFINITY : (m + lg2_approx(lsum) - kAttn4PBias) * 0.69314718055994531f;
   };

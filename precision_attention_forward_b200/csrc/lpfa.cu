@@ -1012,8 +1012,18 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "norm and rotation backward launch");
   if (rows) {
-    lpfa::qk_norm_rope_dw_kernel<<<dim3(rows, 4), 1024, 0, s>>>(p.partials, blocks, rows, p.w_rows[0], dq_weight, dk_weight);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows), 4);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, lpfa::qk_norm_rope_dw_kernel, static_cast<const float*>(p.partials), blocks, rows,
+                           p.w_rows[0], dq_weight, dk_weight);
+    if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
   }
   return LPFA_OK;
 }

@@ -661,6 +661,7 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
   const uint32_t ring = smem_u32(sums + 4 * kRopeWarps) + warp * 2 * kStage;
+  cudaTriggerProgrammaticLaunchCompletion();  // every block runs at once: the sums may be set up already
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int64_t last = min(first + p.tile, p.tokens);
   const int part_rows = p.w_rows[0] + p.w_rows[1];
@@ -847,6 +848,7 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
 __global__ void __launch_bounds__(1024)
 qk_norm_rope_dw_kernel(const float* partials, int blocks, int rows, int rows_q, float* dwq, float* dwk) {
   __shared__ float sums[32][33];
+  cudaGridDependencySynchronize();  // launched while the backward kernel ends
   const int row = blockIdx.x, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int ch = blockIdx.y * 32 + lane;
   float s = 0.f;
