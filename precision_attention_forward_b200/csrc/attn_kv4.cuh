@@ -261,7 +261,8 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
   lim_min = min(lim_min, __shfl_xor_sync(0xFFFFFFFFu, lim_min, 2));
 
   float o[kTiles][8][4];
-  float mx[kTiles][2], l[kTiles][2];
+  // Reference, offset of the exponent (0 while every s is -inf), sum of P.
+  float mx[kTiles][2], off[kTiles][2], l[kTiles][2];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
@@ -269,9 +270,11 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
     mx[n][0] = mx[n][1] = -INFINITY;
+    off[n][0] = off[n][1] = 0.f;
     l[n][0] = l[n][1] = 0.f;
   }
-  uint32_t vref = 0;  // the largest V scale byte so far, in the four bytes of a word
+  uint32_t vref = 0;  // the largest V scale byte so far
+  uint32_t vbias = (15 + kAttn4VBias) * 0x00010001u;  // from a byte to its factor's exponent field
 
   uint8_t* ring = smem4 + warp * kAttn4Ring;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAttn4Bars);
@@ -367,12 +370,22 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
       const bool there = tile * kAttn4Keys + lane < hi && !((gone >> (lane >> 4)) & 1u);
       const uint32_t kw = there ? *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane) : 0u;
       const uint32_t vw = there ? *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane) : 0u;
-      // V's reference follows the largest byte.
-      const uint32_t larger = __vmaxu4(vw, vref);
-      if (__any_sync(0xFFFFFFFFu, larger != vref)) {
-        const uint32_t big = __reduce_max_sync(0xFFFFFFFFu, max_byte(larger));
-        const int down = static_cast<int>(vref & 0xFFu) - static_cast<int>(big);
-        vref = big * 0x01010101u;
+      // K: 2^e as floats (byte 0, 2^-127, counts as 0).
+      kfac[lane] = make_float4(__uint_as_float((kw << 23) & 0x7F800000u), __uint_as_float((kw << 15) & 0x7F800000u),
+                               __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
+      // V: f16 2^(7 + byte - reference): its exponent field, 0 (the value 0) where that would be below 1.
+      constexpr uint32_t kTop = 15 + kAttn4VBias;  // the field of the reference itself
+      uint32_t f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, vbias, 0u);
+      uint32_t f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, vbias, 0u);
+      // A field above kTop (bit 15 once 2^15 - 1 - kTop is added): the reference follows the largest byte.
+      constexpr uint32_t kOver = (0x7FFFu - kTop) * 0x00010001u;
+      if (__any_sync(0xFFFFFFFFu, ((f02 + kOver) | (f13 + kOver)) & 0x80008000u)) {
+        const uint32_t big = max(vref, __reduce_max_sync(0xFFFFFFFFu, max_byte(vw)));
+        const int down = static_cast<int>(vref) - static_cast<int>(big);
+        vref = big;
+        vbias = (0xFFFFu & (kTop - big)) * 0x00010001u;
+        f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, vbias, 0u);
+        f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, vbias, 0u);
         const float fv = down < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + down) << 23);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
@@ -381,14 +394,8 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][d][i] *= fv;
       }
-      // K: 2^e as floats (byte 0, 2^-127, counts as 0).
-      kfac[lane] = make_float4(__uint_as_float((kw & 0xFFu) << 23), __uint_as_float((kw << 15) & 0x7F800000u),
-                               __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
-      // V: f16 2^(7 + byte - reference), the exponent field, 0 (value 0) where it would be below 1.
-      const uint32_t bias =
-          (0xFFFFu & static_cast<uint32_t>(15 + kAttn4VBias - static_cast<int>(vref & 0xFFu))) * 0x00010001u;
-      const uint32_t f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, bias, 0u) << 10;
-      const uint32_t f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, bias, 0u) << 10;
+      f02 <<= 10;
+      f13 <<= 10;
       vfac_mine[0] = static_cast<uint16_t>(f02);
       vfac_mine[2] = static_cast<uint16_t>(f13);
       vfac_mine[4] = static_cast<uint16_t>(f02 >> 16);
@@ -472,6 +479,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
           m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
           const float f = mx[n][i] == -INFINITY ? 0.f : ex2_approx(mx[n][i] - m);  // no key yet: o and l are 0
           mx[n][i] = m;
+          off[n][i] = m == -INFINITY ? 0.f : kAttn4PBias - m;
           l[n][i] *= f;
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
@@ -485,9 +493,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     uint32_t pb[2][kTiles][2];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
-      // (no key seen so far: m = -inf, and every s of the column is -inf too)
-      const float r0 = mx[n][0] == -INFINITY ? 0.f : kAttn4PBias - mx[n][0];
-      const float r1 = mx[n][1] == -INFINITY ? 0.f : kAttn4PBias - mx[n][1];
+      const float r0 = off[n][0], r1 = off[n][1];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float e0 = ex2_approx(fmaf(s[h][n][0], c2[n][0], r0)), e1 = ex2_approx(fmaf(s[h][n][1], c2[n][1], r1));
@@ -551,7 +557,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
   // the cluster's. Rows that do not exist are left out.
   const int real = min(kRows, rows - row0);
   float* part = reinterpret_cast<float*>(ring);  // [kRows][kPitch], then m[kRows], l[kRows]
-  const int undo = static_cast<int>(vref & 0xFFu) - 127 - kAttn4VBias;
+  const int undo = static_cast<int>(vref) - 127 - kAttn4VBias;
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
