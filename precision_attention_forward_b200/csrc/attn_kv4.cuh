@@ -359,6 +359,9 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     ahead = entries(next + kAttn4Warps);
     if (!mbar_wait(&bars[st], phase, nullptr)) {
       if (atomicCAS(&g_lpfa_status[0], 0, 4 /* LPFA_ERR_TIMEOUT */) == 0) atomicExch(&g_lpfa_status[1], kKv4AttnWaitSite);
+      // Every copy under way has to land before this memory is used again or the block ends (bounded too).
+      for (int k = 0; k < kAttn4Stages && tile + k * kAttn4Warps < tile1; ++k)
+        mbar_wait(&bars[(st + k) % kAttn4Stages], phase ^ (st + k >= kAttn4Stages ? 1u : 0u), nullptr);
       break;
     }
 

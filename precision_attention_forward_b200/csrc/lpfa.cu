@@ -928,7 +928,7 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   p.cu_seqlens = meta->dev;
   p.scale_off = meta->dev + meta->num_seqs + 1;
   p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
-  if (meta->total_scale_blocks > INT32_MAX / 16) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
+  if (meta->total_scale_blocks > INT32_MAX / 32) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
   DeviceInfo info;
   if ((st = require_sm100(&info)) != LPFA_OK) return st;
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
@@ -1111,7 +1111,7 @@ lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* ta
   if (!aligned16(k_payload) || !aligned16(k_scales) || !aligned16(v_payload) || !aligned16(v_scales))
     return fail(LPFA_ERR_INVALID_ARG, "payload and scales must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(start) % 4) return fail(LPFA_ERR_INVALID_ARG, "start is misaligned");
-  if (meta->total_scale_blocks > INT32_MAX / 16) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
+  if (meta->total_scale_blocks > INT32_MAX / 32) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
   p.payload[0] = k_payload;
   p.payload[1] = v_payload;
   p.scales[0] = k_scales;
