@@ -557,27 +557,28 @@ class _Scope:
         return self.empty(x.shape, dtype)
 
 
-def _rows(t: torch.Tensor, name: str, dtype, device, shape=None) -> _Rows:
-    """A (tokens, heads, 128) tensor as an lpfa_rows."""
+def _rows(t: torch.Tensor, name: str, dtype, index: int, shape=None) -> _Rows:
+    """A (tokens, heads, 128) tensor on CUDA device `index` as an lpfa_rows."""
     s = t.shape
-    if len(s) != 3 or s[2] != 128 or 0 in s:
+    if len(s) != 3 or s[2] != 128 or not s[0] or not s[1]:
         raise ValueError("%s must be a (tokens, heads, 128) tensor" % name)
-    if t.dtype != dtype or dtype not in _DTYPE_CODE:
+    if t.dtype is not dtype or dtype not in _DTYPE_CODE:
         raise ValueError("%s must be %s" % (name, dtype if dtype in _DTYPE_CODE else "bf16 or fp32"))
-    if not t.is_cuda or t.device != device:
+    if index < 0 or t.get_device() != index:
         raise ValueError("%s must be on the CUDA device of the other tensors" % name)
     if shape is not None and s != shape:
         raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    n, h, _ = s
     a, b, c = t.stride()
     if c != 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
     # The stride of an axis of one element is never stepped over; it may be anything.
-    return _Rows(t.data_ptr(), a if s[0] > 1 else s[1] * 128, b if s[1] > 1 else 128, s[1])
+    return _Rows(t.data_ptr(), a if n > 1 else h * 128, b if h > 1 else 128, h)
 
 
-def _out_rows(t: torch.Tensor, name: str, dtype, device, shape) -> _Rows:
+def _out_rows(t: torch.Tensor, name: str, dtype, index, shape) -> _Rows:
     """As _rows, for a tensor that is written: its elements must be different memory."""
-    r = _rows(t, name, dtype, device, shape)
+    r = _rows(t, name, dtype, index, shape)
     if t.is_contiguous():
         return r
     lo, hi = sorted(((r.tok_stride, shape[0]), (r.head_stride, shape[1])))
@@ -647,17 +648,17 @@ class RotaryAxes:
         self._ptr = ctypes.pointer(self._c)
 
 
-def _weight(w: torch.Tensor, name: str, heads: int, dtype, device):
+def _weight(w: torch.Tensor, name: str, heads: int, dtype, index: int):
     """(address, stride between heads) of a weight."""
     s = w.shape
-    if (s != (128,) and s != (heads, 128)) or not w.is_contiguous() or w.device != device:
+    if s[-1] != 128 or (len(s) != 1 and s != (heads, 128)) or not w.is_contiguous() or w.get_device() != index:
         raise ValueError("%s must be a contiguous (128,) or (heads, 128) tensor on the device of q" % name)
-    if w.dtype != dtype or dtype not in _DTYPE_CODE:
+    if w.dtype is not dtype or dtype not in _DTYPE_CODE:
         raise ValueError("weights must be bf16 or fp32, both the same")
     return w.data_ptr(), 128 if len(s) == 2 else 0
 
 
-def _norm_rope_op(tokens, device, q_heads, k_heads, positions, rope, q_weight, k_weight, eps, norm) -> _NormRope:
+def _norm_rope_op(tokens, index, q_heads, k_heads, positions, rope, q_weight, k_weight, eps, norm) -> _NormRope:
     if norm and not (0.0 <= eps < float("inf")):
         raise ValueError("eps must be finite and >= 0")
     rotary, pos, pt, pa, p64 = None, None, 0, 0, 0
@@ -667,35 +668,41 @@ def _norm_rope_op(tokens, device, q_heads, k_heads, positions, rope, q_weight, k
         if positions is None:
             raise ValueError("a rotation needs positions")
         s = positions.shape
-        if not 1 <= len(s) <= 2 or s[0] != tokens or (s[1] if len(s) == 2 else 1) < rope.axes:
+        two = len(s) == 2
+        if not 1 <= len(s) <= 2 or s[0] != tokens or (s[1] if two else 1) < rope.axes:
             raise ValueError("positions must be (tokens, axes): %d tokens, %d axes" % (tokens, rope.axes))
-        if positions.dtype == torch.int64:
+        dt = positions.dtype
+        if dt is torch.int64:
             p64 = 1
-        elif positions.dtype != torch.int32:
+        elif dt is not torch.int32:
             raise ValueError("positions must be int32 or int64")
-        if positions.device != device:
+        if positions.get_device() != index:
             raise ValueError("positions must be on the device of q")
-        rotary, pos, pt = rope._ptr, positions.data_ptr(), positions.stride(0)
-        if len(s) == 2:
-            pa = positions.stride(1)
-    qw, qs, kw, ks = None, 0, None, 0
-    first = q_weight if q_weight is not None else k_weight
+        rotary, pos = rope._ptr, positions.data_ptr()
+        if two:
+            pt, pa = positions.stride()
+        else:
+            pt = positions.stride(0)
+    qw, qs, kw, ks, wdt = None, 0, None, 0, torch.bfloat16
     if q_weight is not None:
-        qw, qs = _weight(q_weight, "q_weight", q_heads, first.dtype, device)
+        wdt = q_weight.dtype
+        qw, qs = _weight(q_weight, "q_weight", q_heads, wdt, index)
     if k_weight is not None:
         if not k_heads:
             raise ValueError("k_weight without k")
-        kw, ks = _weight(k_weight, "k_weight", k_heads, first.dtype, device)
-    return _NormRope(rotary, pos, pt, pa, p64, 1 if norm else 0, eps, qw, qs, kw, ks,
-                     0 if first is None else _DTYPE_CODE[first.dtype])
+        if q_weight is None:
+            wdt = k_weight.dtype
+        kw, ks = _weight(k_weight, "k_weight", k_heads, wdt, index)
+    return _NormRope(rotary, pos, pt, pa, p64, 1 if norm else 0, eps, qw, qs, kw, ks, _DTYPE_CODE[wdt])
 
 
-def _qk_rows(q, k):
+def _qk_rows(q, k, index):
     """lpfa_rows of q and (None without it) k, and the number of k's heads."""
-    qr = _rows(q, "q", q.dtype, q.device)
+    dt = q.dtype
+    qr = _rows(q, "q", dt, index)
     if k is None:
         return qr, None, 0
-    kr = _rows(k, "k", q.dtype, q.device)
+    kr = _rows(k, "k", dt, index)
     if k.shape[0] != q.shape[0]:
         raise ValueError("q and k must have the same tokens")
     return qr, kr, kr.heads
@@ -714,19 +721,20 @@ def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Opt
     (heads, 128), bf16 or fp32. norm=False leaves the norm out (the weight still applies).
     Outputs: out_dtype (the input's by default), contiguous unless given; an output may be its own input.
     """
-    qr, kr, k_heads = _qk_rows(q, k)
+    index = q.get_device()
+    qr, kr, k_heads = _qk_rows(q, k, index)
     device, dt, shape = q.device, q.dtype, q.shape
     odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE_CODE:
         raise ValueError("out_dtype must be bf16 or fp32")
-    op = _norm_rope_op(shape[0], device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
+    op = _norm_rope_op(shape[0], index, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
     ko = None
     with _Scope(device, stream) as sc:
         if q_out is None:
             q_out = sc.like(q, odt)
             qo = _Rows(q_out.data_ptr(), shape[1] * 128, 128, shape[1])
         else:
-            qo = _out_rows(q_out, "q_out", odt, device, shape)
+            qo = _out_rows(q_out, "q_out", odt, index, shape)
         if k is None:
             if k_out is not None:
                 raise ValueError("k_out without k")
@@ -734,7 +742,7 @@ def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Opt
             k_out = sc.like(k, odt)
             ko = _Rows(k_out.data_ptr(), k_heads * 128, 128, k_heads)
         else:
-            ko = _out_rows(k_out, "k_out", odt, device, k.shape)
+            ko = _out_rows(k_out, "k_out", odt, index, k.shape)
         _check(_lib.lpfa_qk_norm_rope(qr, kr, _DTYPE_CODE[dt], shape[0], 128, op, qo, ko, _DTYPE_CODE[odt], sc.handle))
     return q_out, k_out
 
@@ -748,7 +756,8 @@ def lpfa_qk_norm_rope_mxfp8(q: torch.Tensor, k: Optional[torch.Tensor], position
     """lpfa_qk_norm_rope straight into the attention's input: returns (q_payload, q_scales, k_payload,
     k_scales) as lpfa_quantize_mxfp8_varlen lays them out (None for k without k). The bytes are those
     of lpfa_qk_norm_rope with fp32 outputs and the quantizer after it."""
-    qr, kr, k_heads = _qk_rows(q, k)
+    index = q.get_device()
+    qr, kr, k_heads = _qk_rows(q, k, index)
     device, dt, T = q.device, q.dtype, q.shape[0]
     if T != meta.total_tokens:
         raise ValueError("q has %d tokens but the metadata describes %d" % (T, meta.total_tokens))
@@ -757,7 +766,7 @@ def lpfa_qk_norm_rope_mxfp8(q: torch.Tensor, k: Optional[torch.Tensor], position
     if k is None and (k_payload is not None or k_scales is not None):
         raise ValueError("k_payload or k_scales without k")
     _check_meta_device(meta, device)
-    op = _norm_rope_op(T, device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
+    op = _norm_rope_op(T, index, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
     with _Scope(device, stream) as sc:
         q_payload, q_scales = _mxfp8_out(sc, q, meta, q_payload, q_scales, "q")
         kp = ks = None
@@ -795,20 +804,21 @@ def lpfa_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], 
     for bf16); q, k and the rest as in the forward call. Weight gradients are fp32 in the weight's
     shape. dq may be dq_out's memory, dk dk_out's. Equal calls give equal bits.
     """
-    qr, kr, k_heads = _qk_rows(q, k)
+    index = q.get_device()
+    qr, kr, k_heads = _qk_rows(q, k, index)
     device, dt, shape = q.device, q.dtype, q.shape
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out come together")
-    gq = _rows(dq_out, "dq_out", dt, device, shape)
-    gk = _rows(dk_out, "dk_out", dt, device, k.shape) if k is not None else None
-    op = _norm_rope_op(shape[0], device, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
+    gq = _rows(dq_out, "dq_out", dt, index, shape)
+    gk = _rows(dk_out, "dk_out", dt, index, k.shape) if k is not None else None
+    op = _norm_rope_op(shape[0], index, qr.heads, k_heads, positions, rope, q_weight, k_weight, eps, norm)
     with _Scope(device, stream) as sc:
         dq = sc.like(q, dt) if dq is None else dq
-        dqr = _out_rows(dq, "dq", dt, device, shape)
+        dqr = _out_rows(dq, "dq", dt, index, shape)
         dkr = None
         if k is not None:
             dk = sc.like(k, dt) if dk is None else dk
-            dkr = _out_rows(dk, "dk", dt, device, k.shape)
+            dkr = _out_rows(dk, "dk", dt, index, k.shape)
         elif dk is not None:
             raise ValueError("dk without k")
         dws = []
@@ -866,20 +876,22 @@ class Kv4Cache:
         self._c = _Kv4Cache(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), *k.shape[:3])
 
 
-def _page_table(t: torch.Tensor, num_seqs: int, device) -> _PageTable:
+def _page_table(t: torch.Tensor, num_seqs: int, index: int) -> _PageTable:
     s = t.shape
-    if t.dtype != torch.int32 or len(s) != 2 or s[0] != num_seqs or s[1] < 1 or (s[1] > 1 and t.stride(1) != 1):
-        raise ValueError("page_table must be an int32 (sequences, pages) tensor with contiguous rows: %d sequences"
-                         % num_seqs)
-    if t.device != device:
+    if t.dtype is not torch.int32 or len(s) != 2 or s[0] != num_seqs or s[1] < 1:
+        raise ValueError("page_table must be an int32 (sequences, pages) tensor: %d sequences" % num_seqs)
+    a, b = t.stride()
+    if b != 1 and s[1] > 1:
+        raise ValueError("page_table must have contiguous rows")
+    if t.get_device() != index:
         raise ValueError("page_table must be on the device of the cache")
-    return _PageTable(t.data_ptr(), t.stride(0), s[1])
+    return _PageTable(t.data_ptr(), a, s[1])
 
 
-def _seq_ints(t: Optional[torch.Tensor], name: str, num_seqs: int, device) -> Optional[int]:
+def _seq_ints(t: Optional[torch.Tensor], name: str, num_seqs: int, index: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.shape != (num_seqs,) or not t.is_contiguous() or t.device != device:
+    if t.dtype is not torch.int32 or t.shape != (num_seqs,) or not t.is_contiguous() or t.get_device() != index:
         raise ValueError("%s must be a contiguous int32 tensor of %d sequences on the device of the cache" % (name, num_seqs))
     return t.data_ptr()
 
@@ -894,8 +906,9 @@ def lpfa_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, page_table
     and reported by lpfa_device_status. Two tokens of a call must not share a slot.
     """
     device = cache.device
-    kr = _rows(k, "k", k.dtype, device)
-    vr = _rows(v, "v", k.dtype, device, k.shape)
+    index = device.index
+    kr = _rows(k, "k", k.dtype, index)
+    vr = _rows(v, "v", k.dtype, index, k.shape)
     if k.shape[1] != cache.heads:
         raise ValueError("k has %d heads, the cache %d" % (k.shape[1], cache.heads))
     if k.shape[0] != meta.total_tokens:
@@ -903,8 +916,9 @@ def lpfa_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, page_table
     if scaling_mode not in SCALING_MODES:
         raise ValueError("scaling_mode must be 'rceil' or 'floor'")
     _check_meta_device(meta, device)
-    table = _page_table(page_table, meta.num_seqs, device)
-    starts = _seq_ints(start, "start", meta.num_seqs, device)
+    num_seqs = meta.num_seqs
+    table = _page_table(page_table, num_seqs, device.index)
+    starts = _seq_ints(start, "start", num_seqs, device.index)
     with _Scope(device, stream) as sc:
         _check(_lib.lpfa_kv4_write(kr, vr, _DTYPE_CODE[k.dtype], 128, cache._c, table, starts, meta._c,
                                    SCALING_MODES[scaling_mode], sc.handle))
@@ -918,8 +932,9 @@ def lpfa_kv4_read(cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta, s
     lpfa_attn_fwd_varlen (pv_mode "bf16") or lpfa_dequantize_mxfp8_varlen."""
     device = cache.device
     _check_meta_device(meta, device)
-    table = _page_table(page_table, meta.num_seqs, device)
-    starts = _seq_ints(start, "start", meta.num_seqs, device)
+    num_seqs = meta.num_seqs
+    table = _page_table(page_table, num_seqs, device.index)
+    starts = _seq_ints(start, "start", num_seqs, device.index)
     shape, nb = (meta.total_tokens, cache.heads, 128), (meta.total_scale_blocks * cache.heads * 512,)
     u8 = torch.uint8
     with _Scope(device, stream) as sc:
@@ -944,17 +959,19 @@ def lpfa_attn_fwd_kv4(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor
     for lpfa_kv4_write. For chunks of many query tokens, lpfa_kv4_read and lpfa_attn_fwd_varlen are faster.
     """
     device = cache.device
-    qr = _rows(q, "q", torch.bfloat16, device)
+    index = device.index
+    qr = _rows(q, "q", torch.bfloat16, index)
     Tq, H = q.shape[0], q.shape[1]
     if H % cache.heads:
         raise ValueError("%d query heads are not a multiple of the cache's %d" % (H, cache.heads))
     if Tq != meta_q.total_tokens:
         raise ValueError("q has %d tokens but the metadata describes %d" % (Tq, meta_q.total_tokens))
     _check_meta_device(meta_q, device)
-    table = _page_table(page_table, meta_q.num_seqs, device)
+    num_seqs = meta_q.num_seqs
+    table = _page_table(page_table, num_seqs, index)
     if kv_lens is None:
         raise ValueError("kv_lens is needed")
-    lens = _seq_ints(kv_lens, "kv_lens", meta_q.num_seqs, device)
+    lens = _seq_ints(kv_lens, "kv_lens", num_seqs, index)
     with _Scope(device, stream) as sc:
         if out is None:
             out = sc.like(q, torch.bfloat16)

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -78,10 +79,24 @@ lpfa_status current_device(DeviceInfo* info, int* dev_out = nullptr) {
   return LPFA_OK;
 }
 
-lpfa_status require_sm100(DeviceInfo* info) {
-  lpfa_status st = current_device(info);
+lpfa_status require_sm100(DeviceInfo* info, int* dev = nullptr) {
+  lpfa_status st = current_device(info, dev);
   if (st != LPFA_OK) return st;
   if (!info->sm100) return fail(LPFA_ERR_UNSUPPORTED, "the current device is not sm_100 (B200)");
+  return LPFA_OK;
+}
+
+// Raises a kernel's dynamic shared memory limit (and allows clusters beyond the portable size) once per
+// device: the attributes stay, and setting them costs as much as a tenth of a small call.
+struct KernelLimits {
+  std::atomic<bool> set[kMaxDevices] = {};
+};
+lpfa_status set_limits(KernelLimits& k, const void* fn, int dev, int smem, bool clusters) {
+  if (k.set[dev].load(std::memory_order_acquire)) return LPFA_OK;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  k.set[dev].store(true, std::memory_order_release);
   return LPFA_OK;
 }
 
@@ -851,19 +866,31 @@ int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
 }  // namespace
 
 extern "C++" {
-template <int kOut>
-static lpfa_status launch_rope(bool fp32, bool half, dim3 grid, const lpfa::RopeParams& p,
-                               const lpfa::RopePlan& plan, void* stream) {
-  auto kernel = fp32 ? (half ? lpfa::qk_norm_rope_kernel<float, kOut, true> : lpfa::qk_norm_rope_kernel<float, kOut, false>)
-                     : (half ? lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, true>
-                             : lpfa::qk_norm_rope_kernel<__nv_bfloat16, kOut, false>);
-  const int smem = fp32 ? lpfa::rope_smem_bytes<float>() : lpfa::rope_smem_bytes<__nv_bfloat16>();
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  kernel<<<grid, lpfa::kRopeThreads, static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)>>>(p, plan);
-  e = cudaGetLastError();
+namespace {
+
+template <typename T, int kOut, bool kHalf>
+lpfa_status launch_rope_kernel(dim3 grid, int dev, const lpfa::RopeParams& p, const lpfa::RopePlan& plan, void* stream) {
+  static KernelLimits limits;
+  auto kernel = lpfa::qk_norm_rope_kernel<T, kOut, kHalf>;
+  constexpr int smem = lpfa::rope_smem_bytes<T>();
+  const lpfa_status st = set_limits(limits, reinterpret_cast<const void*>(kernel), dev, smem, false);
+  if (st != LPFA_OK) return st;
+  kernel<<<grid, lpfa::kRopeThreads, smem, static_cast<cudaStream_t>(stream)>>>(p, plan);
+  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation launch");
 }
+
+template <int kOut>
+lpfa_status launch_rope(bool fp32, bool half, dim3 grid, int dev, const lpfa::RopeParams& p, const lpfa::RopePlan& plan,
+                        void* stream) {
+  if (fp32)
+    return half ? launch_rope_kernel<float, kOut, true>(grid, dev, p, plan, stream)
+                : launch_rope_kernel<float, kOut, false>(grid, dev, p, plan, stream);
+  return half ? launch_rope_kernel<__nv_bfloat16, kOut, true>(grid, dev, p, plan, stream)
+              : launch_rope_kernel<__nv_bfloat16, kOut, false>(grid, dev, p, plan, stream);
+}
+
+}  // namespace
 }  // extern "C++"
 
 lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int64_t tokens,
@@ -886,7 +913,8 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
     p.t[i].out_head = out[i]->head_stride;
   }
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   p.quad = rope_quad(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
   p.tiles = static_cast<int>((tokens + ntok - 1) / ntok);
@@ -900,8 +928,8 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
   const dim3 grid(static_cast<unsigned>(std::min(p.tiles, slots)),
                   static_cast<unsigned>((batches + p.batches - 1) / p.batches));
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
-  return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, p, plan, stream)
-                                : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, p, plan, stream);
+  return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, dev, p, plan, stream)
+                                : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, dev, p, plan, stream);
 }
 
 lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt, int32_t head_dim,
@@ -930,23 +958,45 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
   if (meta->total_scale_blocks > INT32_MAX / 32) return fail(LPFA_ERR_INVALID_ARG, "too many tiles");
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   p.quad = rope_quad(p);
   p.batches = rope_batches(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
   p.tiles = meta->total_scale_blocks * (128 / ntok);
   return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half,
-                                       dim3(static_cast<unsigned>(std::min(p.tiles, 2 * info.sms))), p, plan, stream);
+                                       dim3(static_cast<unsigned>(std::min(p.tiles, 2 * info.sms))), dev, p, plan,
+                                       stream);
 }
 
 extern "C++" {
-template <typename T>
-static auto rope_bwd_kernel(bool half, bool per_head) {
-  return half ? (per_head ? lpfa::qk_norm_rope_bwd_kernel<T, true, true> : lpfa::qk_norm_rope_bwd_kernel<T, true, false>)
-              : (per_head ? lpfa::qk_norm_rope_bwd_kernel<T, false, true>
-                          : lpfa::qk_norm_rope_bwd_kernel<T, false, false>);
+namespace {
+
+template <typename T, bool kHalf, bool kPerHead>
+lpfa_status launch_rope_bwd_kernel(int blocks, int dev, const lpfa::RopeParams& p, const lpfa::RopePlan& plan,
+                                   cudaStream_t s) {
+  static KernelLimits limits;
+  auto kernel = lpfa::qk_norm_rope_bwd_kernel<T, kHalf, kPerHead>;
+  constexpr int smem = lpfa::rope_bwd_smem<T>();
+  const lpfa_status st = set_limits(limits, reinterpret_cast<const void*>(kernel), dev, smem, false);
+  if (st != LPFA_OK) return st;
+  kernel<<<blocks, lpfa::kRopeThreads, smem, s>>>(p, plan);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation backward launch");
 }
+
+template <typename T>
+lpfa_status launch_rope_bwd(bool half, bool per_head, int blocks, int dev, const lpfa::RopeParams& p,
+                            const lpfa::RopePlan& plan, cudaStream_t s) {
+  if (half)
+    return per_head ? launch_rope_bwd_kernel<T, true, true>(blocks, dev, p, plan, s)
+                    : launch_rope_bwd_kernel<T, true, false>(blocks, dev, p, plan, s);
+  return per_head ? launch_rope_bwd_kernel<T, false, true>(blocks, dev, p, plan, s)
+                  : launch_rope_bwd_kernel<T, false, false>(blocks, dev, p, plan, s);
+}
+
+}  // namespace
 }  // extern "C++"
 
 size_t lpfa_qk_norm_rope_bwd_workspace_bytes(int32_t q_heads, int32_t k_heads, const lpfa_norm_rope* op) {
@@ -995,22 +1045,18 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
       return fail(LPFA_ERR_INVALID_ARG, "workspace of %zu bytes is too small (%zu needed)", workspace_bytes, need);
   }
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   p.partials = static_cast<float*>(workspace);
   p.tile = static_cast<int>((tokens + lpfa::kRopeBwdBlocks - 1) / lpfa::kRopeBwdBlocks);
   const int blocks = static_cast<int>((tokens + p.tile - 1) / p.tile);
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   p.quad = rope_quad(p);
   const bool per_head = p.w_rows[0] > 1 || p.w_rows[1] > 1;
-  auto kernel = dt == LPFA_IN_FP32 ? rope_bwd_kernel<float>(half, per_head)
-                                   : rope_bwd_kernel<__nv_bfloat16>(half, per_head);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int smem = dt == LPFA_IN_FP32 ? lpfa::rope_bwd_smem<float>() : lpfa::rope_bwd_smem<__nv_bfloat16>();
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  kernel<<<blocks, lpfa::kRopeThreads, static_cast<size_t>(smem), s>>>(p, plan);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation backward launch");
+  st = dt == LPFA_IN_FP32 ? launch_rope_bwd<float>(half, per_head, blocks, dev, p, plan, s)
+                          : launch_rope_bwd<__nv_bfloat16>(half, per_head, blocks, dev, p, plan, s);
+  if (st != LPFA_OK) return st;
   if (rows) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows), 4);
@@ -1021,7 +1067,7 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, lpfa::qk_norm_rope_dw_kernel, static_cast<const float*>(p.partials), blocks, rows,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lpfa::qk_norm_rope_dw_kernel, static_cast<const float*>(p.partials), blocks, rows,
                            p.w_rows[0], dq_weight, dk_weight);
     if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
   }
@@ -1087,7 +1133,8 @@ lpfa_status lpfa_kv4_write(const lpfa_rows* k, const lpfa_rows* v, lpfa_in_dtype
   p.tokens = meta->total_tokens;
   p.floor_mode = mode == LPFA_SCALE_FLOOR ? 1 : 0;
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   // One token per block while there are few, else up to 32 that share their table lookups.
   p.tile = std::min(lpfa::kKv4Tile, (p.tokens + 4 * info.sms - 1) / (4 * info.sms));
   const dim3 grid(static_cast<unsigned>((p.tokens + p.tile - 1) / p.tile), 2);
@@ -1121,7 +1168,8 @@ lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* ta
   p.scale_off = meta->dev + meta->num_seqs + 1;
   p.start = start;
   DeviceInfo info;
-  if ((st = require_sm100(&info)) != LPFA_OK) return st;
+  int dev = 0;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * 4u, 2);
   const int smem = cache->heads * lpfa::kKv4Tile * 4;  // up to 128 KB
   cudaError_t e = cudaSuccess;
@@ -1157,9 +1205,9 @@ template <int kTiles>
 lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, int dev, cudaStream_t s) {
   constexpr uint32_t smem = lpfa::attn4_smem_bytes<kTiles>();
   auto kernel = lpfa::attn_kv4_kernel<kTiles>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  static KernelLimits limits;
+  const lpfa_status st = set_limits(limits, reinterpret_cast<const void*>(kernel), dev, static_cast<int>(smem), true);
+  if (st != LPFA_OK) return st;
   const int64_t tiles = (max_rows + 8 * kTiles - 1) / (8 * kTiles);
   const int64_t work = tiles * p.c.heads * p.num_seqs;
   if (work > INT32_MAX / lpfa::kAttn4MaxSplit) return fail(LPFA_ERR_INVALID_ARG, "too many query tiles");
@@ -1188,7 +1236,7 @@ lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, int
   // Blocks that have to wait for others' places run in order of length (64 ragged sequences of up to
   // 8192 keys: 80 instead of 106 us).
   p.sorted = p.num_seqs > 1 && p.num_seqs <= lpfa::kAttn4SortMax && work * p.splits > 2 * sms;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache attention launch");
 }
 
@@ -1225,7 +1273,7 @@ lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_k
   if (max_rows > INT32_MAX / 2) return fail(LPFA_ERR_INVALID_ARG, "too many query rows in a sequence");
   DeviceInfo info;
   int dev = 0;
-  if ((st = require_sm100(&info)) != LPFA_OK || (st = current_device(&info, &dev)) != LPFA_OK) return st;
+  if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // One row costs what eight do. Sixteen per block halve the conversions and the reads of the cache,
   // with half as many warps on an SM: worth it for more than eight rows, where the largest split still
