@@ -1,7 +1,8 @@
 /*
  * lpfa.h -- C ABI of the block-scaled low-precision FlashAttention forward library
  * (MXFP8 quantization of packed variable-length Q/K/V followed by a noncausal
- * head-dim-128 multi-head attention forward with online softmax, BF16 O and fp32 LSE).
+ * head-dim-128 multi-head attention forward with online softmax, BF16 O and fp32 LSE; its
+ * backward; the norm and rotation of Q and K before it; a paged MXFP4 cache and its attention).
  *
  * Conventions shared by every call
  * --------------------------------

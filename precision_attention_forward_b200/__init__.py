@@ -1,4 +1,5 @@
-"""Python binding of liblpfa: MXFP8 varlen quantization and block-scaled attention forward.
+"""Python binding of liblpfa: MXFP8 varlen quantization, block-scaled attention forward and backward,
+the norm and rotation of Q and K before them, and a paged MXFP4 key/value cache with its attention.
 
 Argument marshalling only: every step of the path runs in the library's CUDA kernels
 (``liblpfa.so``, built in-tree for sm_100a). PyTorch provides device memory and streams.
