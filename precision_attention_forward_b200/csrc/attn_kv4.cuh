@@ -317,15 +317,13 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     const int64_t row1 =
         ((static_cast<int64_t>(pg.y) * p.c.heads + kvh) << p.c.page_shift) + ((key0 + 16) & (p.c.page_size - 1));
     mbar_arrive_expect_tx(&bars[st], (kAttn4StageBytes / 2) * (has0 + has1), leader);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!(h ? has1 : has0)) continue;
-      const int64_t row = h ? row1 : row0;
-      bulk_load(dst + 1024 * h, p.c.payload[0] + row * 64, 1024, &bars[st], leader);
-      bulk_load(dst + 2048 + 1024 * h, p.c.payload[1] + row * 64, 1024, &bars[st], leader);
-      bulk_load(dst + 4096 + 64 * h, p.c.scales[0] + row * 4, 64, &bars[st], leader);
-      bulk_load(dst + 4224 + 64 * h, p.c.scales[1] + row * 4, 64, &bars[st], leader);
-    }
+    // Lanes 0 and 1 fetch a half each.
+    const uint32_t fetch = lane == 0 ? has0 : lane == 1 ? has1 : 0u;
+    const int64_t row = lane ? row1 : row0;
+    bulk_load(dst + 1024 * lane, p.c.payload[0] + row * 64, 1024, &bars[st], fetch);
+    bulk_load(dst + 2048 + 1024 * lane, p.c.payload[1] + row * 64, 1024, &bars[st], fetch);
+    bulk_load(dst + 4096 + 64 * lane, p.c.scales[0] + row * 4, 64, &bars[st], fetch);
+    bulk_load(dst + 4224 + 64 * lane, p.c.scales[1] + row * 4, 64, &bars[st], fetch);
     const uint32_t missing = (key0 < hi && !has0 ? 1u : 0u) | (key0 + 16 < hi && !has1 ? 2u : 0u);
     if (missing && lane == 0) kv4_bad_entry(kKv4AttnPageSite);
     return missing;
