@@ -532,6 +532,8 @@ class _Scope:
             stream = self.other
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            elif stream.device != self.device:
+                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
             self.other = None
             if stream.cuda_stream != self.handle:
                 self.caller = torch.cuda.current_stream()
