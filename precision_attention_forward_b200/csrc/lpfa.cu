@@ -1275,12 +1275,13 @@ lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_k
   int dev = 0;
   if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // One row costs what eight do. Sixteen per block halve the conversions and the reads of the cache,
-  // with half as many warps on an SM: worth it for more than eight rows, where the largest split still
-  // fills the card (16 rows: 32 x 8192 keys 70 instead of 80 us, but 4 x 65536 keys 116 instead of 81).
-  const int64_t work16 = (max_rows + 15) / 16 * p.c.heads * p.num_seqs;
-  return max_rows <= 8 || work16 * 8 < 2 * info.sms ? launch_attn_kv4<1>(p, max_rows, info.sms, dev, s)
-                                                    : launch_attn_kv4<2>(p, max_rows, info.sms, dev, s);
+  // One row costs what eight do. Sixteen per block cost 5/3 as much as eight (conversions and reads of the
+  // cache are shared) with half as many warps on an SM: taken where that is less work for the longest
+  // sequence's rows, and where the largest split still fills the card. (16 rows: 32 x 8192 keys 65
+  // instead of 80 us, but 4 x 65536 keys 116 instead of 74; 20 rows of 8 x 4096 keys 23 instead of 20.)
+  const int64_t tiles16 = (max_rows + 15) / 16, tiles8 = (max_rows + 7) / 8;
+  const bool sixteen = 5 * tiles16 < 3 * tiles8 && tiles16 * p.c.heads * p.num_seqs * 8 >= 2 * info.sms;
+  return sixteen ? launch_attn_kv4<2>(p, max_rows, info.sms, dev, s) : launch_attn_kv4<1>(p, max_rows, info.sms, dev, s);
 }
 
 lpfa_status lpfa_device_status(void* stream, int32_t* detail) {
