@@ -18,7 +18,7 @@
 // The weight is folded into the rotation (w_a cos, w_b sin, ...) once per token, for all heads. The
 // angles depend on the token alone: a warp computes its token's once. An angle is a product in FP64
 // reduced by one FMA to a rest of at most an eighth of a turn (exact up to the frequency's own
-// rounding), so far positions keep their accuracy; sincospif does the rest.
+// rounding), so far positions keep their accuracy, and short series do the rest.
 // Measured (B200): that case 126 us, the time of a device copy of its bytes; 8192 tokens x 32 heads of
 // BF16 into MXFP8 31 us, where 270 warp instructions a step bound it (4 rows: norm and rotation 150,
 // block maxima, scale bytes and conversion 120) and 1024 tiles for 296 blocks leave a ragged last round;
@@ -316,8 +316,17 @@ __device__ __forceinline__ float2 rope_turn(int64_t n, double f) {
   // Quarter turns, and a rest in [-1/8, 1/8] of a turn whose FP32 rounding is below 2^-28.
   const double quarters = rint(pos * f * 4.0);
   const float rest = static_cast<float>(fma(pos, f, -0.25 * quarters));
-  float s, c;
-  sincospif(2.f * rest, &s, &c);
+  // sin and cos of at most pi / 4: the Taylor series to x^9 and x^10 (the next terms are below 2^-29).
+  const float x = 6.28318530718f * rest, x2 = x * x;
+  float s = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(x2, s, 1.f / 120.f);
+  s = fmaf(x2, s, -1.f / 6.f);
+  s = fmaf(x * x2, s, x);
+  float c = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+  c = fmaf(x2, c, -1.f / 720.f);
+  c = fmaf(x2, c, 1.f / 24.f);
+  c = fmaf(x2, c, -0.5f);
+  c = fmaf(x2, c, 1.f);
   const int q = static_cast<int>(static_cast<long long>(quarters)) & 3;
   const float co = (q & 1) ? s : c, si = (q & 1) ? c : s;
   return make_float2((q == 1 || q == 2) ? -co : co, q >= 2 ? -si : si);
@@ -432,21 +441,23 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   constexpr int kLaneElems = sizeof(TIn) == 2 ? 8 : 4;  // elements of a copy
   int rd_tile = blockIdx.x, rd_batch = b0, rd_left = 0;
   uint32_t rd_stage = 0;
-  int64_t rd_tok = 0, rd_step = 0;
+  Place rd_place = {}, coming = {};  // where the loads are; of the tile whose first batch was loaded last
+  int64_t rd_step = 0;
   const TIn* rd = nullptr;
   auto rd_enter = [&](int which, int step) {
     const RopeTensor& t = p.t[which];
-    rd = static_cast<const TIn*>(t.x) + rd_tok * t.tok_stride + (step * heads_per_step + head0) * t.head_stride + kLaneElems * j;
+    rd = static_cast<const TIn*>(t.x) + rd_place.tok * t.tok_stride + (step * heads_per_step + head0) * t.head_stride + kLaneElems * j;
     rd_step = heads_per_step * t.head_stride;
     rd_left = steps_of[which] - step;
   };
-  auto rd_start = [&](int64_t tok) {
-    rd_tok = tok;
+  auto rd_start = [&]() {
+    rd_place = place(rd_tile);
     rd_batch = b0;
     if (b0 < batches_q) rd_enter(0, b0 * kBatch); else rd_enter(1, (b0 - batches_q) * kBatch);
   };
   auto issue = [&]() {
     if (rd_tile < p.tiles) {
+      if (rd_batch == b0) coming = rd_place;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (u < rd_left) {
@@ -459,7 +470,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       rd_stage = rd_stage + kStageBytes == kStages * kStageBytes ? 0 : rd_stage + kStageBytes;
       if (++rd_batch == b1) {
         rd_tile += gridDim.x;
-        if (rd_tile < p.tiles) rd_start(place(rd_tile).tok);
+        if (rd_tile < p.tiles) rd_start();
       } else if (rd_batch == batches_q) {
         rd_enter(1, 0);
       }
@@ -468,7 +479,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   };
   const uint32_t up = p.floor_mode ? 0u : kE4m3Up;
   if (rd_tile >= p.tiles) return;
-  rd_start(place(rd_tile).tok);
+  rd_start();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue();
   const LaneTurns turns = lane_turns(p, plan, lane);
@@ -481,7 +492,8 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
 
 #pragma unroll 1
   for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const Place now = place(tile);
+    static_assert(kStages == 2, "the loads are one batch ahead: in this tile, then in the next one's first");
+    const Place now = coming;
     // The angles of the warp's tokens.
     __syncwarp();  // the previous ones have been read
 #pragma unroll 1
@@ -865,7 +877,7 @@ qk_norm_rope_dw_kernel(const float* partials, int blocks, int rows, int rows_q, 
 #pragma unroll
   for (int i = 0; i < (kRopeBwdBlocks + 31) / 32; ++i) {
     const int b = grp + 32 * i;
-    if (b < blocks) s += __ldg(partials + (static_cast<int64_t>(b) * rows + row) * 128 + ch);
+    if (b < blocks) s += __ldcg(partials + (static_cast<int64_t>(b) * rows + row) * 128 + ch);
   }
   sums[grp][lane] = s;
   __syncthreads();
