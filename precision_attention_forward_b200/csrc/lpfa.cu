@@ -977,7 +977,7 @@ template <typename T, bool kHalf, bool kPerHead>
 lpfa_status launch_rope_bwd_kernel(int blocks, int dev, const lpfa::RopeParams& p, const lpfa::RopePlan& plan,
                                    cudaStream_t s) {
   static KernelLimits limits;
-  auto kernel = lpfa::qk_norm_rope_bwd_kernel<T, kHalf, kPerHead>;
+  auto kernel = kPerHead ? lpfa::qk_norm_rope_bwd_heads_kernel<T, kHalf> : lpfa::qk_norm_rope_bwd_kernel<T, kHalf>;
   constexpr int smem = lpfa::rope_bwd_smem<T>();
   const lpfa_status st = set_limits(limits, reinterpret_cast<const void*>(kernel), dev, smem, false);
   if (st != LPFA_OK) return st;
@@ -986,14 +986,32 @@ lpfa_status launch_rope_bwd_kernel(int blocks, int dev, const lpfa::RopeParams& 
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "norm and rotation backward launch");
 }
 
+// One kernel over p's tensors, and the sums of the weight gradients behind it.
 template <typename T>
-lpfa_status launch_rope_bwd(bool half, bool per_head, int blocks, int dev, const lpfa::RopeParams& p,
-                            const lpfa::RopePlan& plan, cudaStream_t s) {
+lpfa_status launch_rope_bwd(bool half, bool per_head, int dev, const lpfa::RopeParams& p, const lpfa::RopePlan& plan,
+                            float* dwq, float* dwk, cudaStream_t s) {
+  const int blocks = static_cast<int>((p.tokens + p.tile - 1) / p.tile);
+  lpfa_status st;
   if (half)
-    return per_head ? launch_rope_bwd_kernel<T, true, true>(blocks, dev, p, plan, s)
-                    : launch_rope_bwd_kernel<T, true, false>(blocks, dev, p, plan, s);
-  return per_head ? launch_rope_bwd_kernel<T, false, true>(blocks, dev, p, plan, s)
+    st = per_head ? launch_rope_bwd_kernel<T, true, true>(blocks, dev, p, plan, s)
+                  : launch_rope_bwd_kernel<T, true, false>(blocks, dev, p, plan, s);
+  else
+    st = per_head ? launch_rope_bwd_kernel<T, false, true>(blocks, dev, p, plan, s)
                   : launch_rope_bwd_kernel<T, false, false>(blocks, dev, p, plan, s);
+  const int rows = p.w_rows[0] + p.w_rows[1];
+  if (st != LPFA_OK || rows == 0) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows), 4);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lpfa::qk_norm_rope_dw_kernel, static_cast<const float*>(p.partials),
+                                           blocks, rows, p.w_rows[0], dwq, dwk);
+  return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "weight gradient launch");
 }
 
 }  // namespace
@@ -1036,8 +1054,7 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
     if (p.w_rows[i] && (!dw[i] || !aligned16(dw[i])))
       return fail(LPFA_ERR_INVALID_ARG, "%s must be a 16-byte aligned buffer", i ? "dk_weight" : "dq_weight");
   }
-  const int rows = p.w_rows[0] + p.w_rows[1];
-  const size_t need = static_cast<size_t>(rows) * 128u * sizeof(float) * lpfa::kRopeBwdBlocks;
+  const size_t need = lpfa_qk_norm_rope_bwd_workspace_bytes(q->heads, p.t[1].heads, op);
   if (need) {
     if (!workspace || !aligned16(workspace))
       return fail(LPFA_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
@@ -1047,29 +1064,26 @@ lpfa_status lpfa_qk_norm_rope_bwd(const lpfa_rows* dq_out, const lpfa_rows* dk_o
   DeviceInfo info;
   int dev = 0;
   if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
-  p.partials = static_cast<float*>(workspace);
-  p.tile = static_cast<int>((tokens + lpfa::kRopeBwdBlocks - 1) / lpfa::kRopeBwdBlocks);
-  const int blocks = static_cast<int>((tokens + p.tile - 1) / p.tile);
-  const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   p.quad = rope_quad(p);
-  const bool per_head = p.w_rows[0] > 1 || p.w_rows[1] > 1;
+  p.tile = static_cast<int>((tokens + lpfa::kRopeBwdBlocks - 1) / lpfa::kRopeBwdBlocks);
+  const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = dt == LPFA_IN_FP32 ? launch_rope_bwd<float>(half, per_head, blocks, dev, p, plan, s)
-                          : launch_rope_bwd<__nv_bfloat16>(half, per_head, blocks, dev, p, plan, s);
-  if (st != LPFA_OK) return st;
-  if (rows) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows), 4);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, lpfa::qk_norm_rope_dw_kernel, static_cast<const float*>(p.partials), blocks, rows,
-                           p.w_rows[0], dq_weight, dk_weight);
-    if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+  // The tensors with one weight row (or none) in one kernel, those with a row per head in another; as a
+  // rule both are of one kind.
+  float* partials = static_cast<float*>(workspace);
+  for (int per_head = 0; per_head < 2; ++per_head) {
+    lpfa::RopeParams mine = p;
+    for (int i = 0; i < 2; ++i) {
+      if ((p.w_rows[i] > 1) == (per_head != 0)) continue;
+      mine.t[i].heads = 0;
+      mine.w_rows[i] = 0;
+    }
+    if (mine.t[0].heads + mine.t[1].heads == 0) continue;
+    mine.partials = partials;
+    partials += static_cast<int64_t>(mine.w_rows[0] + mine.w_rows[1]) * 128 * lpfa::kRopeBwdBlocks;
+    st = dt == LPFA_IN_FP32 ? launch_rope_bwd<float>(half, per_head != 0, dev, mine, plan, dq_weight, dk_weight, s)
+                            : launch_rope_bwd<__nv_bfloat16>(half, per_head != 0, dev, mine, plan, dq_weight, dk_weight, s);
+    if (st != LPFA_OK) return st;
   }
   return LPFA_OK;
 }

@@ -51,6 +51,11 @@ constexpr int kRopeBwdTile = 64;             // tokens whose angles a backward b
 // Backward blocks, and with them rows of weight-gradient partials: two for each of 148 SMs.
 constexpr int kRopeBwdBlocks = 296;
 
+template <typename T> constexpr int rope_bwd_stage() { return 2 * 4 * 128 * static_cast<int>(sizeof(T)); }
+template <typename T> constexpr int rope_bwd_smem() {
+  return kRopeBwdTile * 128 * 4 + 4 * kRopeWarps * 128 * 4 + kRopeWarps * 2 * rope_bwd_stage<T>();
+}
+
 enum RopeOut : int { kRopeBf16 = 0, kRopeF32 = 1, kRopeMxfp8 = 2 };
 
 // The rotation: frequencies in turns (radians / 2 pi) for a position step of 1, FP64.
@@ -659,23 +664,101 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   cp_async_wait<0>();
 }
 
-// Backward (8192 tokens x 32 heads of BF16 with one weight row: 41 us and 3 for the sums, 1.3 times the
-// copy time of its bytes; 93 warp instructions a row and the three-shuffle sums bound it). Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step
-// (four rows, as in the forward pass) that go round the warps, each with the next one on the way in its
-// shared-memory ring. With one weight row for all heads a lane's sums for its 16 channels stay in
-// registers to the end. With a row per head the block takes one step of heads at a time, and the
-// warps' sums go through shared memory to the block's own row of partials. No atomics: the same sums in
-// the same order every time.
-template <typename T> constexpr int rope_bwd_stage() { return 2 * 4 * 128 * static_cast<int>(sizeof(T)); }
-template <typename T> constexpr int rope_bwd_smem() {
-  return kRopeBwdTile * 128 * 4 + 4 * kRopeWarps * 128 * 4 + kRopeWarps * 2 * rope_bwd_stage<T>();
+// The backward pass of four rows (a step): d becomes dx, and acc gains the weight's gradient where `on`.
+template <typename T, bool kHalf>
+__device__ __forceinline__ void rope_bwd_step(const RopeParams& p, uint32_t rows, const float2* cs, const Pairs& w,
+                                              bool on, int lane, F2 (&acc)[8], Pairs& d) {
+  const int j = lane & 7;
+  const F2 minus = f2(-1.f, -1.f);
+  RawRow<T> rx, rg;
+  rx.load_shared(rows, lane);
+  rg.load_shared(rows + rope_bwd_stage<T>() / 2, lane);
+  float u[8], v[8];
+  rg.get(0, u);
+  rg.get(1, v);
+  Pairs g = to_pairs<kHalf>(u, v);
+  rx.get(0, u);
+  rx.get(1, v);
+  const Pairs x = to_pairs<kHalf>(u, v);
+  F2 ss = f2(0.f, 0.f), hx = f2(0.f, 0.f);
+  F2 gx[8];
+  F2 c[4], sn[4];
+  turn_pairs<kHalf>(cs, j, c, sn);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // Back by the angle: g_a = dy_a c + dy_b s, g_b = dy_b c - dy_a s.
+    const F2 a = f2_fma(g.a[i], c[i], f2_mul(g.b[i], sn[i]));
+    const F2 b = f2_fma(g.b[i], c[i], f2_mul(f2_mul(g.a[i], minus), sn[i]));
+    g.a[i] = a;
+    g.b[i] = b;
+    gx[i] = f2_mul(a, x.a[i]);
+    gx[4 + i] = f2_mul(b, x.b[i]);
+    hx = f2_fma(gx[i], w.a[i], hx);
+    hx = f2_fma(gx[4 + i], w.b[i], hx);
+    ss = f2_fma(x.a[i], x.a[i], ss);
+    ss = f2_fma(x.b[i], x.b[i], ss);
+  }
+  float r = 1.f, q = 0.f;  // dx = r g w + q x
+  if (p.norm) {
+    r = rsqrt_newton(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
+    q = row_sum(f2_sum(hx)) * (-1.f / 128.f) * r * r * r;
+  }
+  const F2 r2 = f2(r, r), q2 = f2(q, q);
+  const F2 ra = on ? r2 : f2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[i] = f2_fma(gx[i], ra, acc[i]);
+    acc[4 + i] = f2_fma(gx[4 + i], ra, acc[4 + i]);
+    d.a[i] = f2_fma(f2_mul(g.a[i], w.a[i]), r2, f2_mul(x.a[i], q2));
+    d.b[i] = f2_fma(f2_mul(g.b[i], w.b[i]), r2, f2_mul(x.b[i], q2));
+  }
 }
 
-template <typename T, bool kHalf, bool kPerHead>
+// A step's rows of x and dy (token `at`, head `head`) into a stage of the warp's ring.
+template <typename T>
+__device__ __forceinline__ void rope_bwd_load(const RopeTensor& t, int64_t at, int head, uint32_t stage, int lane) {
+  constexpr int kLaneElems = sizeof(T) == 2 ? 8 : 4;  // elements of a copy
+  const int e = kLaneElems * (lane & 7);
+  row_async(stage, static_cast<const T*>(t.x) + at * t.tok_stride + head * t.head_stride + e, lane);
+  row_async(stage + rope_bwd_stage<T>() / 2, static_cast<const T*>(t.dy) + at * t.dy_tok + head * t.dy_head + e, lane);
+}
+
+template <typename T, bool kHalf>
+__device__ __forceinline__ void rope_bwd_store(const RopeTensor& t, int64_t at, int head, const Pairs& d, int j) {
+  float u[8], v[8];
+  from_pairs<kHalf>(d, u, v);
+  T* dst = static_cast<T*>(t.out) + at * t.out_tok + head * t.out_head + 8 * j;
+  chunk_store(dst, u);
+  chunk_store(dst + 64, v);
+}
+
+__device__ __forceinline__ void clear(F2 (&acc)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
+}
+
+// The angles of a block's next tokens, by all warps; ends with a barrier.
+__device__ __forceinline__ void rope_bwd_angles(const RopeParams& p, const LaneTurns& turns, float2 (*cs)[64],
+                                                int64_t tok0, int ntok) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int s = warp; s < ntok; s += kRopeWarps) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      cs[s][lane + 32 * i] = rope_turn(rope_position(p, (tok0 + s) * p.pos_tok + turns.axis[i]), turns.f[i]);
+  }
+  __syncthreads();
+}
+
+// Backward with at most one weight row for all heads (8192 tokens x 32 heads of BF16: 41 us and 3 for the
+// sums, 1.3 times the copy time of its bytes; 93 warp instructions a row and the three-shuffle sums
+// bound it). Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step (four
+// rows, as in the forward pass) that go round the warps, each with the next one on the way in its
+// shared-memory ring. A lane's sums for its 16 channels stay in registers to the end. No atomics: the same
+// sums in the same order every time.
+template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
   constexpr int kStage = rope_bwd_stage<T>();
-  constexpr int kLaneElems = sizeof(T) == 2 ? 8 : 4;  // elements of a copy
   extern __shared__ __align__(16) uint8_t rope_smem[];
   float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);                               // [kRopeBwdTile]
   float(*sums)[128] = reinterpret_cast<float(*)[128]>(rope_smem + kRopeBwdTile * 128 * 4);  // [4 * kRopeWarps]
@@ -685,28 +768,13 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
   cudaTriggerProgrammaticLaunchCompletion();  // every block runs at once: the sums may be set up already
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int64_t last = min(first + p.tile, p.tokens);
-  const int part_rows = p.w_rows[0] + p.w_rows[1];
-  float* part = p.partials + static_cast<int64_t>(blockIdx.x) * part_rows * 128;
+  float* part = p.partials + static_cast<int64_t>(blockIdx.x) * (p.w_rows[0] + p.w_rows[1]) * 128;
   const int heads_per_step = p.quad ? 4 : 1;
   const int head0 = p.quad ? grp : 0;
   const int per_place = p.quad ? 1 : 4;
   const int in_place = p.quad ? 0 : grp;
-  const F2 minus = f2(-1.f, -1.f);
   const LaneTurns turns = lane_turns(p, plan, lane);
-
-  // One weight row: the warps' sums join here. (Rows and channels of `sums` as the lanes hold them.)
-  auto put_sums = [&](const F2 (&acc)[8]) {
-    Pairs v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v.a[i] = acc[i];
-      v.b[i] = acc[4 + i];
-    }
-    float x[8], y[8];
-    from_pairs<kHalf>(v, x, y);
-    chunk_store(&sums[warp * 4 + grp][8 * j], x);
-    chunk_store(&sums[warp * 4 + grp][64 + 8 * j], y);
-  };
+  bool turned = false;  // one tile of tokens: its angles serve Q and K
 
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
@@ -714,151 +782,211 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
     if (t.heads == 0) continue;
     const int steps = t.heads / heads_per_step;  // (quad: multiples of four)
     F2 acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
-    Pairs w = weight_pairs<kHalf>(p, t, 0, j);
+    clear(acc);
+    const Pairs w = weight_pairs<kHalf>(p, t, 0, j);
     for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
       const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
-      const int places = (ntok + per_place - 1) / per_place;
-      if (last - first > kRopeBwdTile) __syncthreads();  // the angles of the previous tokens have been read
-#pragma unroll 1
-      for (int outer = 0; outer < (kPerHead ? steps : 1); ++outer) {
-        // This warp's items: (place, step) number warp, warp + 8, ..., steps fastest; or (per head) the
-        // places warp, warp + 8, ... of one step.
-        const int all = kPerHead ? places : places * steps;
-        // An item's rows of x and dy into a stage; a token that does not exist reads the last one there is
-        // and counts for nothing.
-        auto issue = [&](int place, int step, int stage) {
-          const int64_t at = tok0 + min(place * per_place + in_place, ntok - 1);
-          const int head = step * heads_per_step + head0;
-          const T* x = static_cast<const T*>(t.x) + at * t.tok_stride + head * t.head_stride + kLaneElems * j;
-          const T* dy = static_cast<const T*>(t.dy) + at * t.dy_tok + head * t.dy_head + kLaneElems * j;
-          row_async(ring + stage * kStage, x, lane);
-          row_async(ring + stage * kStage + kStage / 2, dy, lane);
-        };
-        // The item after (place, step).
-        auto advance = [&](int& place, int& step) {
-          if (kPerHead) {
-            place += kRopeWarps;
-          } else {
-            step += kRopeWarps;
-            while (step >= steps) {
-              step -= steps;
-              ++place;
-            }
-          }
-        };
-        int place = kPerHead ? warp : 0, step = kPerHead ? outer : warp;
-        if (!kPerHead) {
-          step -= kRopeWarps;
-          advance(place, step);
+      const int all = (ntok + per_place - 1) / per_place * steps;
+      // This warp's items: (place, step) number warp, warp + 8, ..., steps fastest.
+      int place = 0, step = warp;
+      auto settle = [&]() {
+        while (step >= steps) {
+          step -= steps;
+          ++place;
         }
-        if (warp < all) issue(place, step, 0);
-        cp_async_commit();
-        if (outer == 0 && (which == 0 || last - first > kRopeBwdTile)) {  // else Q's angles are still there
-          for (int s = warp; s < ntok; s += kRopeWarps) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              cs[s][lane + 32 * i] = rope_turn(rope_position(p, (tok0 + s) * p.pos_tok + turns.axis[i]), turns.f[i]);
-          }
-          __syncthreads();
-        }
-        if (kPerHead && t.w_head != 0) w = weight_pairs<kHalf>(p, t, outer * heads_per_step + head0, j);
-        int stage = 0;
-#pragma unroll 1
-        for (int it = warp; it < all; it += kRopeWarps, stage ^= 1) {
-          const int s = place * per_place + in_place;
-          const int head = step * heads_per_step + head0;
-          const bool on = s < ntok;
-          if (sizeof(T) == 4) __syncwarp();  // the stage to fill has been read (FP32: by other lanes too)
-          advance(place, step);
-          if (it + kRopeWarps < all) issue(place, step, stage ^ 1);
-          cp_async_commit();
-          cp_async_wait<1>();
-          if (sizeof(T) == 4) __syncwarp();
-          RawRow<T> rx, rg;
-          rx.load_shared(ring + stage * kStage, lane);
-          rg.load_shared(ring + stage * kStage + kStage / 2, lane);
-
-          float u[8], v[8];
-          rg.get(0, u);
-          rg.get(1, v);
-          Pairs g = to_pairs<kHalf>(u, v);
-          rx.get(0, u);
-          rx.get(1, v);
-          const Pairs x = to_pairs<kHalf>(u, v);
-          F2 ss = f2(0.f, 0.f), hx = f2(0.f, 0.f);
-          F2 gx[8];
-          F2 c[4], sn[4];
-          turn_pairs<kHalf>(cs[min(s, ntok - 1)], j, c, sn);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // Back by the angle: g_a = dy_a c + dy_b s, g_b = dy_b c - dy_a s.
-            const F2 a = f2_fma(g.a[i], c[i], f2_mul(g.b[i], sn[i]));
-            const F2 b = f2_fma(g.b[i], c[i], f2_mul(f2_mul(g.a[i], minus), sn[i]));
-            g.a[i] = a;
-            g.b[i] = b;
-            gx[i] = f2_mul(a, x.a[i]);
-            gx[4 + i] = f2_mul(b, x.b[i]);
-            hx = f2_fma(gx[i], w.a[i], hx);
-            hx = f2_fma(gx[4 + i], w.b[i], hx);
-            ss = f2_fma(x.a[i], x.a[i], ss);
-            ss = f2_fma(x.b[i], x.b[i], ss);
-          }
-          float r = 1.f, q = 0.f;  // dx = r g w + q x
-          if (p.norm) {
-            r = rsqrt_newton(row_sum(f2_sum(ss)) * (1.f / 128.f) + p.eps);
-            q = row_sum(f2_sum(hx)) * (-1.f / 128.f) * r * r * r;
-          }
-          const F2 r2 = f2(r, r), q2 = f2(q, q);
-          const F2 ra = on ? r2 : f2(0.f, 0.f);
-          Pairs d;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[i] = f2_fma(gx[i], ra, acc[i]);
-            acc[4 + i] = f2_fma(gx[4 + i], ra, acc[4 + i]);
-            d.a[i] = f2_fma(f2_mul(g.a[i], w.a[i]), r2, f2_mul(x.a[i], q2));
-            d.b[i] = f2_fma(f2_mul(g.b[i], w.b[i]), r2, f2_mul(x.b[i], q2));
-          }
-          if (on) {
-            from_pairs<kHalf>(d, u, v);
-            T* dst = static_cast<T*>(t.out) + (tok0 + s) * t.out_tok + head * t.out_head + 8 * j;
-            chunk_store(dst, u);
-            chunk_store(dst + 64, v);
-          }
-        }
-        cp_async_wait<0>();
-        __syncwarp();
-        if (kPerHead && p.w_rows[which] > 1) {
-          put_sums(acc);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = f2(0.f, 0.f);
-          __syncthreads();
-          for (int i = threadIdx.x; i < heads_per_step * 128; i += kRopeThreads) {
-            const int head = outer * heads_per_step + (i >> 7);
-            float sum = 0.f;
-            if (p.quad) {
-#pragma unroll
-              for (int k = 0; k < kRopeWarps; ++k) sum += sums[4 * k + (i >> 7)][i & 127];
-            } else {
-              for (int k = 0; k < 4 * kRopeWarps; ++k) sum += sums[k][i];
-            }
-            float* to = part + (which * p.w_rows[0] + head) * 128 + (i & 127);
-            *to = tok0 == first ? sum : *to + sum;
-          }
-          __syncthreads();
-        }
+      };
+      settle();
+      // A token that does not exist reads the last one there is and counts for nothing.
+      auto load = [&](int stage) {
+        rope_bwd_load<T>(t, tok0 + min(place * per_place + in_place, ntok - 1), step * heads_per_step + head0,
+                         ring + stage * kStage, lane);
+      };
+      if (warp < all) load(0);
+      cp_async_commit();
+      if (!turned) {
+        if (last - first > kRopeBwdTile) __syncthreads();  // the angles of the previous tokens have been read
+        rope_bwd_angles(p, turns, cs, tok0, ntok);
+        turned = last - first <= kRopeBwdTile;
       }
+      int stage = 0;
+#pragma unroll 1
+      for (int it = warp; it < all; it += kRopeWarps, stage ^= 1) {
+        const int s = place * per_place + in_place;
+        const int head = step * heads_per_step + head0;
+        if (sizeof(T) == 4) __syncwarp();  // the stage to fill has been read (FP32: by other lanes too)
+        step += kRopeWarps;
+        settle();
+        if (it + kRopeWarps < all) load(stage ^ 1);
+        cp_async_commit();
+        cp_async_wait<1>();
+        if (sizeof(T) == 4) __syncwarp();
+        Pairs d;
+        rope_bwd_step<T, kHalf>(p, ring + stage * kStage, cs[min(s, ntok - 1)], w, s < ntok, lane, acc, d);
+        if (s < ntok) rope_bwd_store<T, kHalf>(t, tok0 + s, head, d, j);
+      }
+      cp_async_wait<0>();
+      __syncwarp();
     }
     if (p.w_rows[which] == 1) {
       __syncthreads();
-      put_sums(acc);
+      Pairs v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v.a[i] = acc[i];
+        v.b[i] = acc[4 + i];
+      }
+      float x[8], y[8];
+      from_pairs<kHalf>(v, x, y);
+      chunk_store(&sums[warp * 4 + grp][8 * j], x);
+      chunk_store(&sums[warp * 4 + grp][64 + 8 * j], y);
       __syncthreads();
       if (threadIdx.x < 128) {
         float sum = 0.f;
 #pragma unroll 8
         for (int k = 0; k < 4 * kRopeWarps; ++k) sum += sums[k][threadIdx.x];
         part[which * p.w_rows[0] * 128 + threadIdx.x] = sum;
+      }
+    }
+  }
+}
+
+// Backward with a weight row per head. A warp keeps a step (four heads, or one) while it walks the block's
+// tokens, so that a head's sums are complete in its lanes and go straight to the block's row of partials.
+// The steps left when the others have gone round the eight warps evenly are split: a warp takes a
+// part of the tokens, and the parts meet in shared memory (2,740 tokens x 40 FP32 heads: two of the ten
+// steps, in four parts each; 38.6 us with the sums, where a block that took one step at a time
+// over all its warps, with a barrier after each, took 47.9).
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads, 2)
+qk_norm_rope_bwd_heads_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
+  constexpr int kStage = rope_bwd_stage<T>();
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);  // [kRopeBwdTile]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = lane >> 3, j = lane & 7;
+  float(*sums)[128] = reinterpret_cast<float(*)[128]>(rope_smem + kRopeBwdTile * 128 * 4);  // [4 * kRopeWarps]
+  const uint32_t ring = smem_u32(sums + 4 * kRopeWarps) + warp * 2 * kStage;
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
+  const int64_t last = min(first + p.tile, p.tokens);
+  const int part_rows = p.w_rows[0] + p.w_rows[1];
+  const int heads_per_step = p.quad ? 4 : 1;
+  const int head0 = p.quad ? grp : 0;
+  const int per_place = p.quad ? 1 : 4;
+  const int in_place = p.quad ? 0 : grp;
+  const int steps_q = p.t[0].heads / heads_per_step;
+  const int steps = steps_q + p.t[1].heads / heads_per_step;
+  const int whole = steps / kRopeWarps * kRopeWarps;  // steps that go round the warps evenly
+  const int rest = steps - whole;
+  const int splits = rest ? kRopeWarps / rest : 1;  // parts of each of the others: at most one a warp
+  const int units = whole + rest * splits;
+  float* part = p.partials + static_cast<int64_t>(blockIdx.x) * part_rows * 128;
+  const LaneTurns turns = lane_turns(p, plan, lane);
+
+#pragma unroll 1
+  for (int64_t tok0 = first; tok0 < last; tok0 += kRopeBwdTile) {
+    const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
+    const int places = (ntok + per_place - 1) / per_place;
+    if (tok0 != first) __syncthreads();  // the angles of the previous tokens have been read
+    rope_bwd_angles(p, turns, cs, tok0, ntok);
+    // A unit's step and places; a part may have none.
+    auto enter = [&](int unit, int& step, int& place, int& end) {
+      step = unit < whole ? unit : whole + (unit - whole) / splits;
+      const int i = unit < whole ? 0 : (unit - whole) % splits, n = unit < whole ? 1 : splits;
+      place = places * i / n;
+      end = places * (i + 1) / n;
+    };
+    // The rows to load next: the places of one unit after another.
+    int rd_unit = warp, rd_step = 0, rd_place = 0, rd_end = 0;
+    auto rd_enter = [&]() {
+      for (; rd_unit < units; rd_unit += kRopeWarps) {
+        enter(rd_unit, rd_step, rd_place, rd_end);
+        if (rd_place < rd_end) break;
+      }
+    };
+    auto load = [&](int stage) {
+      if (rd_unit < units) {
+        const int step = rd_step;
+        const bool is_k = step >= steps_q;
+        rope_bwd_load<T>(p.t[is_k], tok0 + min(rd_place * per_place + in_place, ntok - 1),
+                         (is_k ? step - steps_q : step) * heads_per_step + head0, ring + stage * kStage, lane);
+        if (++rd_place == rd_end) {
+          rd_unit += kRopeWarps;
+          rd_enter();
+        }
+      }
+      cp_async_commit();
+    };
+    rd_enter();
+    load(0);
+    int stage = 0;
+#pragma unroll 1
+    for (int unit = warp; unit < units; unit += kRopeWarps) {
+      int step, place, end;
+      enter(unit, step, place, end);
+      const bool is_k = step >= steps_q;
+      const RopeTensor& t = p.t[is_k];
+      const int head = (is_k ? step - steps_q : step) * heads_per_step + head0;
+      const Pairs w = weight_pairs<kHalf>(p, t, head, j);
+      F2 acc[8];
+      clear(acc);
+#pragma unroll 1
+      for (; place < end; ++place, stage ^= 1) {
+        const int s = place * per_place + in_place;
+        if (sizeof(T) == 4) __syncwarp();  // the stage to fill has been read (FP32: by other lanes too)
+        load(stage ^ 1);
+        cp_async_wait<1>();
+        if (sizeof(T) == 4) __syncwarp();
+        Pairs d;
+        rope_bwd_step<T, kHalf>(p, ring + stage * kStage, cs[min(s, ntok - 1)], w, s < ntok, lane, acc, d);
+        if (s < ntok) rope_bwd_store<T, kHalf>(t, tok0 + s, head, d, j);
+      }
+      if (!p.quad) {  // the four tokens of a step are one head's
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i].x += __shfl_xor_sync(0xFFFFFFFFu, acc[i].x, 8);
+          acc[i].y += __shfl_xor_sync(0xFFFFFFFFu, acc[i].y, 8);
+          acc[i].x += __shfl_xor_sync(0xFFFFFFFFu, acc[i].x, 16);
+          acc[i].y += __shfl_xor_sync(0xFFFFFFFFu, acc[i].y, 16);
+        }
+      }
+      if (p.quad || grp == 0) {
+        const bool split = unit >= whole && splits > 1;
+        float* to = (split ? sums[4 * warp + grp] : part + ((is_k ? p.w_rows[0] : 0) + head) * 128) + 8 * j;
+        Pairs v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v.a[i] = acc[i];
+          v.b[i] = acc[4 + i];
+        }
+        float x[8], y[8];
+        from_pairs<kHalf>(v, x, y);
+        if (tok0 != first && !split) {  // the same lanes' sums of the tokens before
+          RawRow<float> before;
+          before.load(to);
+          float bx[8], by[8];
+          before.get(0, bx);
+          before.get(1, by);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] += bx[i];
+            y[i] += by[i];
+          }
+        }
+        chunk_store(to, x);
+        chunk_store(to + 64, y);
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    if (splits > 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < rest * heads_per_step * 128; i += kRopeThreads) {
+        const int ch = i & 127, h = (i >> 7) % heads_per_step, r = (i >> 7) / heads_per_step;
+        float sum = 0.f;
+        for (int k = 0; k < splits; ++k) sum += sums[4 * (r * splits + k) + h][ch];
+        float* to = part + ((whole + r) * heads_per_step + h) * 128 + ch;  // (the rows of Q, then those of K)
+        *to = tok0 == first ? sum : *to + sum;
       }
     }
   }

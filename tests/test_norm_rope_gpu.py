@@ -234,6 +234,41 @@ def test_gradients_match_the_oracle(case):
     assert lp.lpfa_device_status() == (lp.LPFA_OK, 0)
 
 
+@pytest.mark.parametrize("case", [
+    # Rows of weights per head: parts of the tokens (some of them empty) and second rounds of 64 tokens a block;
+    # the last two have a row per head on one side and one row on the other.
+    (20011, 3, 1, "fp32", "half", "heads", "heads"), (19200, 8, 4, "bf16", "interleaved", "heads", "heads"),
+    (500, 7, 2, "bf16", "half", "heads", "heads"), (1, 2, 1, "fp32", "half", "heads", "heads"),
+    (700, 12, 8, "fp32", "interleaved", "heads", "heads"), (301, 8, 2, "bf16", "half", "heads", "one"),
+    (1200, 4, 8, "fp32", "half", "one", "heads"),
+])
+def test_weight_gradients_per_head(case):
+    T, hq, hk, dt, pairing, *kinds = case
+    seed = T + hq
+    q, k, w, pos, ang = _case(seed, T, hq, hk, dt, (128,), "heads")
+    w = [x if kind == "heads" else np.ascontiguousarray(x[0]) for x, kind in zip(w, kinds)]
+    g = np.random.default_rng(seed)
+    dq, dk = (_round(g.standard_normal(x.shape), dt) for x in (q, k))
+    rest = (torch.from_numpy(pos).cuda(), lp.RotaryAxes((128,), pairing=pairing), *(_dev(x, dt) for x in w))
+    got = lp.lpfa_qk_norm_rope_bwd(*(_dev(x, dt) for x in (dq, dk, q, k)), *rest)
+    torch.cuda.synchronize()
+    a, b = onr.pair_indices(pairing)
+    for i, (x, dy) in enumerate(((q, dq), (k, dk))):
+        rx, rw, _ = onr.norm_rope_bwd(dy, x, w[i], ang, pairing)
+        h = np.empty(dy.shape)
+        h[..., a] = h[..., b] = np.abs(dy[..., a].astype(np.float64)) + np.abs(dy[..., b])
+        ax = np.abs(x.astype(np.float64))
+        r = 1.0 / np.sqrt((ax * ax).mean(-1, keepdims=True) + 1e-6)
+        hw = h * np.abs(w[i])
+        made = r * hw + ax * r ** 3 * (hw * ax).mean(-1, keepdims=True)  # the bounds of the cases above
+        tol = made * 2.0 ** -19 + (np.abs(rx) * 2.0 ** -8 if dt == "bf16" else 0)
+        assert (np.abs(got[i].double().cpu().numpy() - rx) <= tol).all()
+        terms = (h * ax * r).sum(axis=(0,) if kinds[i] == "heads" else (0, 1))
+        assert got[2 + i].shape == w[i].shape
+        assert (np.abs(got[2 + i].double().cpu().numpy() - rw) <= terms * 2.0 ** -15).all()
+    assert lp.lpfa_device_status() == (lp.LPFA_OK, 0)
+
+
 def test_gradients_are_the_differences_of_the_forward():
     """Central differences of the FP32 forward: truncation (step 2^-6)^2 / 6 of the third derivative and
     2^-20 * 16 / step of rounding; 2e-3 of the gradient's size covers both."""
