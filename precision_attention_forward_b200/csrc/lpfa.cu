@@ -852,11 +852,19 @@ lpfa_status rope_setup(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dtype dt,
 // the former where every head then has its place.
 int rope_quad(const lpfa::RopeParams& p) { return p.t[0].heads % 4 == 0 && p.t[1].heads % 4 == 0; }
 
-int rope_batches(const lpfa::RopeParams& p) {
-  const int per_step = p.quad ? 4 : 1;
-  int n = 0;
-  for (const lpfa::RopeTensor& t : p.t) n += (t.heads / per_step + lpfa::kRopeBatch - 1) / lpfa::kRopeBatch;
-  return n;
+// The forward kernel's items of work for `tiles` tiles, and its grid: two blocks per SM walk the items. All
+// heads of a token share its angles, so a tile is split only where blocks would stand idle.
+dim3 rope_items(lpfa::RopeParams& p, int tiles, int sms) {
+  const int per_step = p.quad ? 4 : 1, slots = 2 * sms;
+  int batches = 0;
+  for (const lpfa::RopeTensor& t : p.t) batches += (t.heads / per_step + lpfa::kRopeBatch - 1) / lpfa::kRopeBatch;
+  p.whole = tiles / slots * slots;
+  const int rest = tiles - p.whole;
+  const int parts = rest ? std::min(batches, slots / rest) : 1;
+  p.batches = (batches + parts - 1) / parts;
+  p.parts = (batches + p.batches - 1) / p.batches;
+  p.items = p.whole + rest * p.parts;
+  return dim3(static_cast<unsigned>(std::min(p.items, slots)));
 }
 
 int rope_weight_rows(const void* w, int64_t head_stride, int heads) {
@@ -917,16 +925,7 @@ lpfa_status lpfa_qk_norm_rope(const lpfa_rows* q, const lpfa_rows* k, lpfa_in_dt
   if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   p.quad = rope_quad(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
-  p.tiles = static_cast<int>((tokens + ntok - 1) / ntok);
-  // Two blocks per SM walk the tiles. All heads of a token share its angles; with fewer tiles than
-  // blocks the heads are split to shorten the call.
-  const int slots = 2 * info.sms;
-  const int batches = rope_batches(p);
-  int parts = 1;
-  while (p.tiles * parts < slots && parts < batches) parts *= 2;
-  p.batches = (batches + parts - 1) / parts;
-  const dim3 grid(static_cast<unsigned>(std::min(p.tiles, slots)),
-                  static_cast<unsigned>((batches + p.batches - 1) / p.batches));
+  const dim3 grid = rope_items(p, static_cast<int>((tokens + ntok - 1) / ntok), info.sms);
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   return out_dt == LPFA_IN_BF16 ? launch_rope<lpfa::kRopeBf16>(dt == LPFA_IN_FP32, half, grid, dev, p, plan, stream)
                                 : launch_rope<lpfa::kRopeF32>(dt == LPFA_IN_FP32, half, grid, dev, p, plan, stream);
@@ -962,12 +961,9 @@ lpfa_status lpfa_qk_norm_rope_mxfp8(const lpfa_rows* q, const lpfa_rows* k, lpfa
   if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   const bool half = op->rotary && op->rotary->pairing == LPFA_PAIR_HALF;
   p.quad = rope_quad(p);
-  p.batches = rope_batches(p);
   const int ntok = p.quad ? lpfa::kRopeWarps : lpfa::kRopeTokens;
-  p.tiles = meta->total_scale_blocks * (128 / ntok);
-  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half,
-                                       dim3(static_cast<unsigned>(std::min(p.tiles, 2 * info.sms))), dev, p, plan,
-                                       stream);
+  const dim3 grid = rope_items(p, meta->total_scale_blocks * (128 / ntok), info.sms);
+  return launch_rope<lpfa::kRopeMxfp8>(dt == LPFA_IN_FP32, half, grid, dev, p, plan, stream);
 }
 
 extern "C++" {

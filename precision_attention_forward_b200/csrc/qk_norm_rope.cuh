@@ -87,9 +87,9 @@ struct RopeParams {
   int w_bf16;  // weights are BF16 (else FP32)
   int norm;
   int quad;  // 1: a warp's four rows are heads of one token; 0: the same head of four tokens
-  int tiles; // forward: tiles of tokens
+  int items, whole, parts;  // forward: items of work; tiles that are one item each; parts of each of the others
   int tile;  // backward: tokens per block in all
-  int batches; // forward: batches of steps (of four rows) per block and token, of those of Q and K together
+  int batches;              // forward: batches of steps of such a part
   // MXFP8 only
   int num_seqs;
   const int32_t* cu_seqlens;
@@ -380,9 +380,11 @@ __device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs
   }
 }
 
-// Grid (blocks, head parts). A warp's four rows are four heads of one token (quad) or, where the head
-// counts are not multiples of four, one head of four tokens; a step is four rows, and blockIdx.y takes
-// p.batches of the batches of Q's steps and then K's. Tiles of 8 (32) tokens go round the blocks:
+// A warp's four rows are four heads of one token (quad) or, where the head
+// counts are not multiples of four, one head of four tokens; a step is four rows, and an item the batches of
+// Q's steps and then K's of a tile of tokens. Items go round the blocks; the tiles left after the last
+// whole round (all of them, in a small call) are split by heads into p.parts items of p.batches batches each, as
+// many as fill the round (8192 tokens x 32 heads into MXFP8, 136 of 1024 tiles in halves: MEASURED). A tile is 8 (32) tokens:
 // consecutive tokens, or for MXFP8 the rows r0, r0 + 1 (.. r0 + 7) of each 32-row quarter of a padded
 // 128-token block, whose scale words fill whole sectors of the atoms between them. The warps are on
 // their own, without a barrier: each computes its tokens' angles while its first rows are on the way,
@@ -407,9 +409,8 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   const float2* my_cs = cs[slot];
 
   struct Place {
-    int64_t tok;     // token; 0 where there is none (read the first, write nothing)
-    int64_t block;   // MXFP8: 128-token block, and the row in it
-    int row;
+    int tok;         // token; 0 where there is none (read the first, write nothing)
+    int block, row;  // MXFP8: 128-token block, and the row in it
     bool real;
   };
   auto place = [&](int tile) {
@@ -419,14 +420,15 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
     if (kOut == kRopeMxfp8) {
       w.block = tile / parts;
       w.row = (tile % parts) * span + in_block;
-      const int seq = find_seq(p.scale_off, p.num_seqs, static_cast<int>(w.block));
+      const int seq = find_seq(p.scale_off, p.num_seqs, w.block);
       const int start = __ldg(p.cu_seqlens + seq);
-      const int64_t in_seq = (w.block - __ldg(p.scale_off + seq)) * 128 + w.row;
-      w.tok = start + in_seq;
+      const int64_t in_seq = static_cast<int64_t>(w.block - __ldg(p.scale_off + seq)) * 128 + w.row;
+      w.tok = static_cast<int>(start + in_seq);
       w.real = in_seq < __ldg(p.cu_seqlens + seq + 1) - start;
     } else {
-      w.tok = static_cast<int64_t>(tile) * ntok + slot;
-      w.real = w.tok < p.tokens;
+      const int64_t tok = static_cast<int64_t>(tile) * ntok + slot;
+      w.tok = static_cast<int>(tok);
+      w.real = tok < p.tokens;
     }
     if (!w.real) w.tok = 0;
     return w;
@@ -438,13 +440,26 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   // (quad: the heads of both are multiples of four)
   const int steps_of[2] = {p.t[0].heads / heads_per_step, p.t[1].heads / heads_per_step};
   const int batches_q = (steps_of[0] + kBatch - 1) / kBatch;
-  const int b0 = blockIdx.y * p.batches;
-  const int b1 = min(batches_q + (steps_of[1] + kBatch - 1) / kBatch, b0 + p.batches);
+  const int batches = batches_q + (steps_of[1] + kBatch - 1) / kBatch;
+  struct Item {
+    int tile, b0, b1;  // batches b0 .. b1 of a tile
+  };
+  auto item_at = [&](int n) {
+    Item it = {n, 0, batches};
+    if (n >= p.whole) {
+      const int part = (n - p.whole) % p.parts;
+      it.tile = p.whole + (n - p.whole) / p.parts;
+      it.b0 = part * p.batches;
+      it.b1 = min(it.b0 + p.batches, batches);
+    }
+    return it;
+  };
 
   // The loads run ahead, batch after batch and tile after tile, into the warp's ring.
   const uint32_t ring = smem_u32(rope_smem) + kRopeTokens * 64 * 8 + warp * kStages * kStageBytes;
   constexpr int kLaneElems = sizeof(TIn) == 2 ? 8 : 4;  // elements of a copy
-  int rd_tile = blockIdx.x, rd_batch = b0, rd_left = 0;
+  int rd_item = blockIdx.x, rd_batch = 0, rd_end = 0, rd_left = 0;
+  bool rd_first = false;
   uint32_t rd_stage = 0;
   Place rd_place = {}, coming = {};  // where the loads are; of the tile whose first batch was loaded last
   int64_t rd_step = 0;
@@ -456,13 +471,17 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
     rd_left = steps_of[which] - step;
   };
   auto rd_start = [&]() {
-    rd_place = place(rd_tile);
-    rd_batch = b0;
-    if (b0 < batches_q) rd_enter(0, b0 * kBatch); else rd_enter(1, (b0 - batches_q) * kBatch);
+    const Item it = item_at(rd_item);
+    rd_place = place(it.tile);
+    rd_batch = it.b0;
+    rd_end = it.b1;
+    rd_first = true;
+    if (it.b0 < batches_q) rd_enter(0, it.b0 * kBatch); else rd_enter(1, (it.b0 - batches_q) * kBatch);
   };
   auto issue = [&]() {
-    if (rd_tile < p.tiles) {
-      if (rd_batch == b0) coming = rd_place;
+    if (rd_item < p.items) {
+      if (rd_first) coming = rd_place;
+      rd_first = false;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (u < rd_left) {
@@ -473,9 +492,9 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       }
       rd_left -= kBatch;
       rd_stage = rd_stage + kStageBytes == kStages * kStageBytes ? 0 : rd_stage + kStageBytes;
-      if (++rd_batch == b1) {
-        rd_tile += gridDim.x;
-        if (rd_tile < p.tiles) rd_start();
+      if (++rd_batch == rd_end) {
+        rd_item += gridDim.x;
+        if (rd_item < p.items) rd_start();
       } else if (rd_batch == batches_q) {
         rd_enter(1, 0);
       }
@@ -483,7 +502,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
     cp_async_commit();
   };
   const uint32_t up = p.floor_mode ? 0u : kE4m3Up;
-  if (rd_tile >= p.tiles) return;
+  if (rd_item >= p.items) return;
   rd_start();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue();
@@ -496,14 +515,16 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   };
 
 #pragma unroll 1
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    static_assert(kStages == 2, "the loads are one batch ahead: in this tile, then in the next one's first");
+  for (int n = blockIdx.x; n < p.items; n += gridDim.x) {
+    static_assert(kStages == 2, "the loads are one batch ahead: in this item, then in the next one's first");
     const Place now = coming;
+    const Item it = item_at(n);
+    const int b0 = it.b0, b1 = it.b1;
     // The angles of the warp's tokens.
     __syncwarp();  // the previous ones have been read
 #pragma unroll 1
     for (int of = 0; of < (p.quad ? 1 : 4); ++of) {
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, now.tok, of * 8);
+      const int at = __shfl_sync(0xFFFFFFFFu, now.tok, of * 8);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         cs[(p.quad ? warp : warp * 4) + of][lane + 32 * i] =
@@ -527,8 +548,8 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       head = step * heads_per_step + head0;
       // Where this lane's row goes: values, or payload bytes and its scale bytes.
       if (kOut == kRopeMxfp8) {
-        sf = t.scales + (now.block * t.heads + head) * 512 + (now.row & 31) * 16 + (now.row >> 5) * 4;
-        bytes = static_cast<uint8_t*>(t.out) + (now.tok * t.heads + head) * 128 + 8 * j;
+        sf = t.scales + (static_cast<int64_t>(now.block) * t.heads + head) * 512 + (now.row & 31) * 16 + (now.row >> 5) * 4;
+        bytes = static_cast<uint8_t*>(t.out) + (static_cast<int64_t>(now.tok) * t.heads + head) * 128 + 8 * j;
       } else if (kOut == kRopeBf16) {
         out16 = static_cast<__nv_bfloat16*>(t.out) + now.tok * t.out_tok + head * t.out_head + 8 * j;
       } else {
