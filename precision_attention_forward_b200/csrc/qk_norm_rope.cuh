@@ -20,9 +20,9 @@
 // reduced by one FMA to a rest of at most an eighth of a turn (exact up to the frequency's own
 // rounding), so far positions keep their accuracy, and short series do the rest.
 // Measured (B200): that case 126 us, the time of a device copy of its bytes; 8192 tokens x 32 heads of
-// BF16 into MXFP8 31 us, where 270 warp instructions a step bound it (4 rows: norm and rotation 150,
-// block maxima, scale bytes and conversion 120) and 1024 tiles for 296 blocks leave a ragged last round;
-// ragged FP32 sequences into MXFP8 at 84 % of the copy bandwidth.
+// BF16 into MXFP8 29 us, where 270 warp instructions a step bound it (4 rows: norm and rotation 150,
+// block maxima, scale bytes and conversion 120); ragged FP32 sequences into MXFP8 at 83 % of the copy
+// bandwidth.
 #pragma once
 
 #include <cstdint>
@@ -88,8 +88,8 @@ struct RopeParams {
   int norm;
   int quad;  // 1: a warp's four rows are heads of one token; 0: the same head of four tokens
   int items, whole, parts;  // forward: items of work; tiles that are one item each; parts of each of the others
-  int tile;  // backward: tokens per block in all
   int batches;              // forward: batches of steps of such a part
+  int tile;                 // backward: tokens per block in all
   // MXFP8 only
   int num_seqs;
   const int32_t* cu_seqlens;
@@ -380,17 +380,17 @@ __device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs
   }
 }
 
-// A warp's four rows are four heads of one token (quad) or, where the head
-// counts are not multiples of four, one head of four tokens; a step is four rows, and an item the batches of
-// Q's steps and then K's of a tile of tokens. Items go round the blocks; the tiles left after the last
-// whole round (all of them, in a small call) are split by heads into p.parts items of p.batches batches each, as
-// many as fill the round (8192 tokens x 32 heads into MXFP8, 136 of 1024 tiles in halves: MEASURED). A tile is 8 (32) tokens:
-// consecutive tokens, or for MXFP8 the rows r0, r0 + 1 (.. r0 + 7) of each 32-row quarter of a padded
-// 128-token block, whose scale words fill whole sectors of the atoms between them. The warps are on
-// their own, without a barrier: each computes its tokens' angles while its first rows are on the way,
-// and loads ahead into its next token. (The other mapping, in which a block's warps share each token's
-// rows and sweep contiguous memory, needs a barrier and an address calculation per item: 167 us for
-// the case that takes 132.)
+// A warp's four rows are four heads of one token (quad) or, where the head counts are not multiples of four,
+// one head of four tokens; a step is four rows, and an item the batches of Q's steps and then K's of
+// a tile of tokens. Items go round the blocks. The tiles left after the last whole round (all of them, in
+// a small call) are split by heads into p.parts items of p.batches batches each, as many as fill the
+// round: 8192 tokens x 32 heads into MXFP8, where 136 of 1024 tiles are left, took 32.8 us with whole tiles and
+// 30.8 with halves. A tile is 8 (32) tokens: consecutive ones, or for MXFP8 the rows r0, r0 + 1
+// (.. r0 + 7) of each 32-row quarter of a padded 128-token block, whose scale words fill whole sectors
+// of the atoms between them. The warps are on their own, without a barrier: each computes its tokens'
+// angles while its first rows are on the way, and loads ahead into its next token. (The other mapping, in
+// which a block's warps share each token's rows and sweep contiguous memory, needs a barrier and an
+// address calculation per item: 167 us for the case that takes 132.)
 template <typename TIn, int kOut, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
