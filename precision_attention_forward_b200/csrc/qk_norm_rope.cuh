@@ -219,9 +219,15 @@ struct Pairs {
   F2 a[4], b[4];
 };
 
+// Lane j's pairs 0 .. 7 are pairs 8 j .. 8 j + 7 of the head (half), or 4 j .. 4 j + 3 and 32 on (interleaved).
+// A token's angles lie in shared memory as the lanes take them: cos and sin of pairs 2 i and 2 i + 1 of lane
+// j are the four floats at 4 (8 i + j), so that eight lanes read 128 bytes in a row and find two pairs
+// side by side. The word of pair p's cos; its sin is two further.
 template <bool kHalf>
-__device__ __forceinline__ int pair_of(int j, int i) {  // i-th pair (0..7) of lane j
-  return kHalf ? 8 * j + i : 4 * j + (i & 3) + 32 * (i >> 2);
+__device__ __forceinline__ int turn_word(int p) {
+  const int j = kHalf ? p >> 3 : (p & 31) >> 2;
+  const int i = kHalf ? p & 7 : (p & 3) + 4 * (p >> 5);
+  return 4 * (8 * (i >> 1) + j) + (i & 1);
 }
 
 template <bool kHalf>
@@ -351,14 +357,20 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// cos and sin of lane j's pairs.
 template <bool kHalf>
-__device__ __forceinline__ void turn_pairs(const float2* cs, int j, F2 (&c)[4], F2 (&s)[4]) {
+__device__ __forceinline__ void put_turn(float* cs, int pair, float2 turn) {
+  float* to = cs + turn_word<kHalf>(pair);
+  to[0] = turn.x;
+  to[2] = turn.y;
+}
+
+// cos and sin of lane j's pairs.
+__device__ __forceinline__ void turn_pairs(const float* cs, int j, F2 (&c)[4], F2 (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(cs + pair_of<kHalf>(j, 2 * i));
-    c[i] = f2(v.x, v.z);
-    s[i] = f2(v.y, v.w);
+    const float4 v = *reinterpret_cast<const float4*>(cs + 4 * (8 * i + j));
+    c[i] = f2(v.x, v.y);
+    s[i] = f2(v.z, v.w);
   }
 }
 
@@ -367,10 +379,10 @@ struct Turn {
   F2 ac[4], bs[4], as[4], bc[4];
 };
 template <bool kHalf>
-__device__ __forceinline__ void make_turn(Turn& m, const float2* cs, const Pairs& w, int j) {
+__device__ __forceinline__ void make_turn(Turn& m, const float* cs, const Pairs& w, int j) {
   const F2 minus = f2(-1.f, -1.f);
   F2 c[4], s[4];
-  turn_pairs<kHalf>(cs, j, c, s);
+  turn_pairs(cs, j, c, s);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     m.ac[i] = f2_mul(w.a[i], c[i]);
@@ -398,7 +410,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   constexpr int kStages = rope_stages<TIn>();
   constexpr int kStageBytes = rope_stage_bytes<TIn>();
   extern __shared__ __align__(16) uint8_t rope_smem[];
-  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);
+  float(*cs)[128] = reinterpret_cast<float(*)[128]>(rope_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
   const int ntok = p.quad ? kRopeWarps : kRopeTokens;
@@ -406,7 +418,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
   const int span = ntok / 4;                        // MXFP8: rows of a quarter
   const int parts = 32 / span;                      // MXFP8: tiles of a 128-token block
   const int in_block = slot % span + 32 * (slot / span);
-  const float2* my_cs = cs[slot];
+  const float* my_cs = cs[slot];
 
   struct Place {
     int tok;         // token; 0 where there is none (read the first, write nothing)
@@ -527,8 +539,8 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
       const int at = __shfl_sync(0xFFFFFFFFu, now.tok, of * 8);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        cs[(p.quad ? warp : warp * 4) + of][lane + 32 * i] =
-            rope_turn(rope_position(p, at * p.pos_tok + turns.axis[i]), turns.f[i]);
+        put_turn<kHalf>(cs[(p.quad ? warp : warp * 4) + of], lane + 32 * i,
+                        rope_turn(rope_position(p, at * p.pos_tok + turns.axis[i]), turns.f[i]));
     }
     __syncwarp();
 
@@ -687,7 +699,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant_
 
 // The backward pass of four rows (a step): d becomes dx, and acc gains the weight's gradient where `on`.
 template <typename T, bool kHalf>
-__device__ __forceinline__ void rope_bwd_step(const RopeParams& p, uint32_t rows, const float2* cs, const Pairs& w,
+__device__ __forceinline__ void rope_bwd_step(const RopeParams& p, uint32_t rows, const float* cs, const Pairs& w,
                                               bool on, int lane, F2 (&acc)[8], Pairs& d) {
   const int j = lane & 7;
   const F2 minus = f2(-1.f, -1.f);
@@ -704,7 +716,7 @@ __device__ __forceinline__ void rope_bwd_step(const RopeParams& p, uint32_t rows
   F2 ss = f2(0.f, 0.f), hx = f2(0.f, 0.f);
   F2 gx[8];
   F2 c[4], sn[4];
-  turn_pairs<kHalf>(cs, j, c, sn);
+  turn_pairs(cs, j, c, sn);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // Back by the angle: g_a = dy_a c + dy_b s, g_b = dy_b c - dy_a s.
@@ -759,13 +771,14 @@ __device__ __forceinline__ void clear(F2 (&acc)[8]) {
 }
 
 // The angles of a block's next tokens, by all warps; ends with a barrier.
-__device__ __forceinline__ void rope_bwd_angles(const RopeParams& p, const LaneTurns& turns, float2 (*cs)[64],
+template <bool kHalf>
+__device__ __forceinline__ void rope_bwd_angles(const RopeParams& p, const LaneTurns& turns, float (*cs)[128],
                                                 int64_t tok0, int ntok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int s = warp; s < ntok; s += kRopeWarps) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      cs[s][lane + 32 * i] = rope_turn(rope_position(p, (tok0 + s) * p.pos_tok + turns.axis[i]), turns.f[i]);
+      put_turn<kHalf>(cs[s], lane + 32 * i, rope_turn(rope_position(p, (tok0 + s) * p.pos_tok + turns.axis[i]), turns.f[i]));
   }
   __syncthreads();
 }
@@ -781,7 +794,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
   constexpr int kStage = rope_bwd_stage<T>();
   extern __shared__ __align__(16) uint8_t rope_smem[];
-  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);                               // [kRopeBwdTile]
+  float(*cs)[128] = reinterpret_cast<float(*)[128]>(rope_smem);                               // [kRopeBwdTile]
   float(*sums)[128] = reinterpret_cast<float(*)[128]>(rope_smem + kRopeBwdTile * 128 * 4);  // [4 * kRopeWarps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
@@ -826,7 +839,7 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
       cp_async_commit();
       if (!turned) {
         if (last - first > kRopeBwdTile) __syncthreads();  // the angles of the previous tokens have been read
-        rope_bwd_angles(p, turns, cs, tok0, ntok);
+        rope_bwd_angles<kHalf>(p, turns, cs, tok0, ntok);
         turned = last - first <= kRopeBwdTile;
       }
       int stage = 0;
@@ -882,7 +895,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_bwd_heads_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
   constexpr int kStage = rope_bwd_stage<T>();
   extern __shared__ __align__(16) uint8_t rope_smem[];
-  float2(*cs)[64] = reinterpret_cast<float2(*)[64]>(rope_smem);  // [kRopeBwdTile]
+  float(*cs)[128] = reinterpret_cast<float(*)[128]>(rope_smem);  // [kRopeBwdTile]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, j = lane & 7;
   float(*sums)[128] = reinterpret_cast<float(*)[128]>(rope_smem + kRopeBwdTile * 128 * 4);  // [4 * kRopeWarps]
@@ -909,7 +922,7 @@ qk_norm_rope_bwd_heads_kernel(const __grid_constant__ RopeParams p, const __grid
     const int ntok = static_cast<int>(min(static_cast<int64_t>(kRopeBwdTile), last - tok0));
     const int places = (ntok + per_place - 1) / per_place;
     if (tok0 != first) __syncthreads();  // the angles of the previous tokens have been read
-    rope_bwd_angles(p, turns, cs, tok0, ntok);
+    rope_bwd_angles<kHalf>(p, turns, cs, tok0, ntok);
     // A unit's step and places; a part may have none.
     auto enter = [&](int unit, int& step, int& place, int& end) {
       step = unit < whole ? unit : whole + (unit - whole) / splits;
