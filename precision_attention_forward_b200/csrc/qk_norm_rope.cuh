@@ -21,8 +21,8 @@
 // rounding), so far positions keep their accuracy, and short series do the rest.
 // Measured (B200): that case 126 us, the time of a device copy of its bytes; 8192 tokens x 32 heads of
 // BF16 into MXFP8 29 us, where 270 warp instructions a step bound it (4 rows: norm and rotation 150,
-// block maxima, scale bytes and conversion 120); ragged FP32 sequences into MXFP8 at 83 % of the copy
-// bandwidth.
+// block maxima, scale bytes and conversion 120); ragged FP32 sequences into MXFP8 at 95 % of the copy
+// bandwidth, and at 85 % once the power limit has lowered the clock.
 #pragma once
 
 #include <cstdint>
@@ -222,7 +222,8 @@ struct Pairs {
 // Lane j's pairs 0 .. 7 are pairs 8 j .. 8 j + 7 of the head (half), or 4 j .. 4 j + 3 and 32 on (interleaved).
 // A token's angles lie in shared memory as the lanes take them: cos and sin of pairs 2 i and 2 i + 1 of lane
 // j are the four floats at 4 (8 i + j), so that eight lanes read 128 bytes in a row and find two pairs
-// side by side. The word of pair p's cos; its sin is two further.
+// side by side (in the order of the pairs, with bank conflicts, the backward pass that takes 43.4 us took
+// 45.0). turn_word: the word of pair p's cos; its sin is two further.
 template <bool kHalf>
 __device__ __forceinline__ int turn_word(int p) {
   const int j = kHalf ? p >> 3 : (p & 31) >> 2;
@@ -783,8 +784,8 @@ __device__ __forceinline__ void rope_bwd_angles(const RopeParams& p, const LaneT
   __syncthreads();
 }
 
-// Backward with at most one weight row for all heads (8192 tokens x 32 heads of BF16: 41 us and 3 for the
-// sums, 1.3 times the copy time of its bytes; 93 warp instructions a row and the three-shuffle sums
+// Backward with at most one weight row for all heads (8192 tokens x 32 heads of BF16: 43.4 us with the
+// sums, 1.4 times the copy time of its bytes; 92 warp instructions a row and the three-shuffle sums
 // bound it). Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step (four
 // rows, as in the forward pass) that go round the warps, each with the next one on the way in its
 // shared-memory ring. A lane's sums for its 16 channels stay in registers to the end. No atomics: the same
@@ -888,7 +889,7 @@ qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, const __grid_const
 // tokens, so that a head's sums are complete in its lanes and go straight to the block's row of partials.
 // The steps left when the others have gone round the eight warps evenly are split: a warp takes a
 // part of the tokens, and the parts meet in shared memory (2,740 tokens x 40 FP32 heads: two of the ten
-// steps, in four parts each; 38.6 us with the sums, where a block that took one step at a time
+// steps, in four parts each; 37.9 us with the sums, where a block that took one step at a time
 // over all its warps, with a barrier after each, took 47.9).
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 2)
