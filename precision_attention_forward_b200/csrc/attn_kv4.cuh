@@ -20,10 +20,20 @@
 // scaled per row by a power of two into FP16's range, which holds a BF16 value exactly down to
 // 2^-29 of the row's largest. O^T = V^T P^T: the fragment's channels lie in one scale block too, so
 // V's scale multiplies P (8 half2 products per 16 keys) and V's codes stay unscaled.
-// P is FP16 with the bias 2^4, relative to a reference that trails the maximum by at most 2^4, and V's
-// scale is relative to the warp's largest one with the bias 2^7: P keeps its 11 bits down to 2^-18 of
-// the largest and vanishes below 2^-28, V's scale is exact down to 2^-21 of the largest and vanishes
-// below that, and their product stays under 2^15. S, the softmax statistics and O are FP32.
+//
+// Range. P is FP16 with the bias 2^10, relative to a reference that trails the maximum by at most 2^4. V's
+// scale is an FP16 power of two relative to a unit, one for each of the four channel blocks, which the warp
+// takes from its first tile; the window of scales from 2^-15 to 2^0 of the unit becomes 2^-14 to 2^1, and the
+// product of both is at most 2^15. A weight keeps its 11 bits down to 2^-24 of the reference, and its product
+// down to 2^-25 of the largest that the window allows; below that a product is off by at most 2^-35 of the
+// largest weight times the largest scale: 2^-20 of the row's largest p 2^e (e: the scale) at worst, since the key of
+// the reference has a scale in the window too.
+// With a scale outside the window neither holds: a large one that the row does not see or hardly weighs would take the
+// others' bits. From such a tile on, the warp joins P and V's scale in FP32 and rounds once, relative to the
+// tile's largest p 2^e in each row and channel block (attn4_wide). That costs up to 1.8 times the tame form:
+// 64 ragged sequences of up to 8192 keys with scales over 30 binades at random take 118 instead of 69 us.
+// O is FP32 in the block's unit, with room for 2^60 above it, where the unit moves, and 2^100 below.
+// S and the softmax statistics are FP32.
 //
 // Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and
 // accumulators (no barrier in the loop); one lane fetches the tiles ahead by bulk copies, two to six
@@ -60,8 +70,10 @@ constexpr int kAttn4Ring = kAttn4Bars + 16 * ((kAttn4Stages + 1) / 2);
 constexpr int kAttn4MaxSplit = 16;  // blocks of a cluster
 constexpr int kAttn4SortMax = 512;  // sequences that are put in order
 constexpr float kAttn4Lag = 4.f;    // binades that the running maximum may be exceeded by
-constexpr float kAttn4PBias = 4.f;  // P is 2^4 e^(s - m), at most 2^8
-constexpr int kAttn4VBias = 7;      // V's scale is 2^(7 + byte - largest byte)
+constexpr int kAttn4PBias = 10;     // P is 2^10 e^(s - m), at most 2^14
+constexpr int kAttn4VBias = 1;      // V's scale is 2^(1 + byte - unit), at most 2^1
+constexpr int kAttn4VRoom = 4;      // the unit is the first tile's largest byte and this much more, for the tiles after it
+constexpr int kAttn4VAbove = 60;    // a byte further above the unit moves it
 
 struct Attn4Params {
   Kv4Cache c;
@@ -120,6 +132,17 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The units of V's scales in channel blocks 0 and 2 (word 0) or 1 and 3 (word 1) as a packed addend: byte +
+// (15 - unit) is a byte's place in the window, 0 to 15.
+__device__ __forceinline__ uint32_t v_addend(int unit_lo, int unit_hi) {
+  return static_cast<uint32_t>(15 - unit_lo) + (static_cast<uint32_t>(15 - unit_hi) << 16);
+}
+__device__ __forceinline__ void v_units(uint32_t addend, int& unit_lo, int& unit_hi) {
+  const int lo = static_cast<int16_t>(addend & 0xFFFFu);
+  unit_lo = 15 - lo;
+  unit_hi = 15 - (static_cast<int32_t>(addend - static_cast<uint32_t>(lo)) >> 16);
+}
+
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -130,17 +153,90 @@ __device__ __forceinline__ float dsmem_ld(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// The largest of a word's four bytes.
-__device__ __forceinline__ uint32_t max_byte(uint32_t w) {
-  w = __vmaxu4(w, w >> 16);
-  return max(w & 0xFFu, (w >> 8) & 0xFFu);
-}
-
 // Physical key of row m (0..7) of an 8-row half of a fragment: 0 5 1 4 2 7 3 6. With it the eight rows
 // that a quarter warp reads for K fall into different banks, and V's reads take two passes for four.
 __device__ __forceinline__ int attn4_key(int m) { return (m & 1) ? 4 + ((m >> 1) ^ 1) : m >> 1; }
 // And back: the row of the fragment that holds key k (0..7).
 __device__ __forceinline__ int attn4_row(int k) { return k < 4 ? 2 * k : 2 * ((k - 4) ^ 1) + 1; }
+
+// The softmax and O^T += V^T P^T of a tile where V's scales lie far apart (see the head of the file): with z
+// the exponent of P, the weight of a key in a channel block is 2^(z + byte + kAttn4VBias - unit), and goes in
+// relative to the tile's largest one in its row. Rare, so short before fast.
+template <int kTiles>
+__device__ __forceinline__ void attn4_wide(const uint8_t* kt, int lane, const uint32_t (&vadd)[2],
+                                           float (&s)[2][kTiles][4], const float (&c2)[kTiles][2],
+                                           const float (&off)[kTiles][2], float (&l)[kTiles][2],
+                                           float (&o)[kTiles][8][4]) {
+  constexpr float kTop = 14.f;  // the largest weight goes in as 2^14
+  const uint8_t* vt = kt + 2048;
+  const int g = lane >> 2, t = lane & 3;
+  int unit[4];
+  v_units(vadd[0], unit[0], unit[2]);
+  v_units(vadd[1], unit[1], unit[3]);
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[h][n][i] = fmaf(s[h][n][i], c2[n][i & 1], off[n][i & 1]);
+        l[n][i & 1] += ex2_approx(s[h][n][i]);
+      }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float by[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        by[h][e] = static_cast<float>(static_cast<int>(kt[4224 + 4 * (16 * h + 8 * e + attn4_key(g)) + b]) + kAttn4VBias - unit[b]);
+    uint32_t pw[2][kTiles][2];
+    float back[kTiles][2];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      float low[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float m = fmaxf(fmaxf(s[0][n][i] + by[0][0], s[0][n][2 + i] + by[0][1]),
+                        fmaxf(s[1][n][i] + by[1][0], s[1][n][2 + i] + by[1][1]));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        back[n][i] = ex2_approx(m - kTop);
+        low[i] = m == -INFINITY ? 0.f : kTop - m;  // no key of the tile: every weight is 2^-inf
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a0 = by[h][0], a1 = by[h][1];
+        pw[h][n][0] = movmatrix(half2_bits(ex2_approx(s[h][n][0] + (a0 + low[0])), ex2_approx(s[h][n][1] + (a0 + low[1]))));
+        pw[h][n][1] = movmatrix(half2_bits(ex2_approx(s[h][n][2] + (a1 + low[0])), ex2_approx(s[h][n][3] + (a1 + low[1]))));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // Byte 2 b + j of the eight of a key that this lane's fragment holds: the codes of two channels.
+        const uint8_t* ra = vt + (16 * h + t) * 64 + g * 8 + 2 * b + j;
+        const uint8_t* rb = vt + (16 * h + 4 + (t ^ 1)) * 64 + g * 8 + 2 * b + j;
+        const uint32_t wa = ra[0], wb = rb[0], wc = ra[512], wd = rb[512];
+        a[h][0] = cvt_e2m1x2_to_f16x2<0>((wa & 0xFu) | (wb << 4));
+        a[h][1] = cvt_e2m1x2_to_f16x2<0>((wa >> 4) | (wb & 0xF0u));
+        a[h][2] = cvt_e2m1x2_to_f16x2<0>((wc & 0xFu) | (wd << 4));
+        a[h][3] = cvt_e2m1x2_to_f16x2<0>((wc >> 4) | (wd & 0xF0u));
+      }
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        float d[4];
+        mma_f16_zero(d, a[0][0], a[0][1], a[0][2], a[0][3], pw[0][n][0], pw[0][n][1]);
+        mma_f16(d, a[1][0], a[1][1], a[1][2], a[1][3], pw[1][n][0], pw[1][n][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][2 * b + j][i] = fmaf(d[i], back[n][i & 1], o[n][2 * b + j][i]);
+      }
+    }
+  }
+}
 
 // kTiles: tiles of 8 query rows that a block holds (rows = query tokens x query heads of a key head).
 template <int kTiles>
@@ -268,8 +364,8 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     off[n][0] = off[n][1] = 0.f;
     l[n][0] = l[n][1] = 0.f;
   }
-  uint32_t vref = 0;  // the largest V scale byte so far
-  uint32_t vbias = (15 + kAttn4VBias) * 0x00010001u;  // from a byte to its factor's exponent field
+  constexpr int kNoUnit = -16384;  // the first tile finds every byte far above its unit
+  uint32_t vadd[2] = {v_addend(kNoUnit, kNoUnit), v_addend(kNoUnit, kNoUnit)};
 
   uint8_t* ring = smem4 + warp * kAttn4Ring;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAttn4Bars);
@@ -342,65 +438,56 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
   int st = 0;
   uint32_t phase = 0;
   int2 ahead = entries(mine + (kAttn4Stages - 1) * kAttn4Warps);  // loaded a tile before they are needed
-#pragma unroll 1
-  for (int tile = mine; tile < tile1; tile += kAttn4Warps) {
+  // The steps of a tile. Refill of the stage before it, and the wait for its own; false: the wait ran out.
+  auto fetch = [&](int tile) {
     __syncwarp();  // the stage to refill, and the factors, have been read
     const int next = tile + (kAttn4Stages - 1) * kAttn4Warps;
     const int nst = st == 0 ? kAttn4Stages - 1 : st - 1;
     bad &= ~(3u << (2 * nst));
     if (next < tile1) bad |= load_tile(next, ahead, nst) << (2 * nst);
     ahead = entries(next + kAttn4Warps);
-    if (!mbar_wait(&bars[st], phase, nullptr)) {
-      if (atomicCAS(&g_lpfa_status[0], 0, 4 /* LPFA_ERR_TIMEOUT */) == 0) atomicExch(&g_lpfa_status[1], kKv4AttnWaitSite);
-      // Every copy under way has to land before this memory is used again or the block ends (bounded too).
-      for (int k = 0; k < kAttn4Stages && tile + k * kAttn4Warps < tile1; ++k)
-        mbar_wait(&bars[(st + k) % kAttn4Stages], phase ^ (st + k >= kAttn4Stages ? 1u : 0u), nullptr);
-      break;
-    }
-
+    if (mbar_wait(&bars[st], phase, nullptr)) return true;
+    if (atomicCAS(&g_lpfa_status[0], 0, 4 /* LPFA_ERR_TIMEOUT */) == 0) atomicExch(&g_lpfa_status[1], kKv4AttnWaitSite);
+    // Every copy under way has to land before this memory is used again or the block ends (bounded too).
+    for (int k = 0; k < kAttn4Stages && tile + k * kAttn4Warps < tile1; ++k)
+      mbar_wait(&bars[(st + k) % kAttn4Stages], phase ^ (st + k >= kAttn4Stages ? 1u : 0u), nullptr);
+    return false;
+  };
+  // Scale words of key `lane` (K's as factors into shared memory: 2^e as floats; byte 0, 2^-127, counts as 0). Keys
+  // beyond hi or without a page have K's scales 0.
+  auto scale_words = [&](int tile, uint32_t gone, bool& there) {
     const uint8_t* kt = ring + st * kAttn4StageBytes;
-    const uint8_t* vt = kt + 2048;
-    const uint32_t gone = (bad >> (2 * st)) & 3u;
-    // ---- factors of key `lane`; keys beyond hi or without a page count as 0
-    {
-      const bool there = tile * kAttn4Keys + lane < hi && !((gone >> (lane >> 4)) & 1u);
-      const uint32_t kw = there ? *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane) : 0u;
-      const uint32_t vw = there ? *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane) : 0u;
-      // K: 2^e as floats (byte 0, 2^-127, counts as 0).
-      kfac[lane] = make_float4(__uint_as_float((kw << 23) & 0x7F800000u), __uint_as_float((kw << 15) & 0x7F800000u),
-                               __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
-      // V: f16 2^(7 + byte - reference): its exponent field, 0 (the value 0) where that would be below 1.
-      constexpr uint32_t kTop = 15 + kAttn4VBias;  // the field of the reference itself
-      uint32_t f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, vbias, 0u);
-      uint32_t f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, vbias, 0u);
-      // A field above kTop (bit 15 once 2^15 - 1 - kTop is added): the reference follows the largest byte.
-      constexpr uint32_t kOver = (0x7FFFu - kTop) * 0x00010001u;
-      if (__any_sync(0xFFFFFFFFu, ((f02 + kOver) | (f13 + kOver)) & 0x80008000u)) {
-        const uint32_t big = max(vref, __reduce_max_sync(0xFFFFFFFFu, max_byte(vw)));
-        const int down = static_cast<int>(vref) - static_cast<int>(big);
-        vref = big;
-        vbias = (0xFFFFu & (kTop - big)) * 0x00010001u;
-        f02 = __viaddmax_s16x2_relu(vw & 0x00FF00FFu, vbias, 0u);
-        f13 = __viaddmax_s16x2_relu((vw >> 8) & 0x00FF00FFu, vbias, 0u);
-        const float fv = down < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + down) << 23);
+    there = tile * kAttn4Keys + lane < hi && !((gone >> (lane >> 4)) & 1u);
+    const uint32_t kw = there ? *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane) : 0u;
+    kfac[lane] = make_float4(__uint_as_float((kw << 23) & 0x7F800000u), __uint_as_float((kw << 15) & 0x7F800000u),
+                             __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
+    return there ? *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane) : 0u;
+  };
+  // The first tile sets V's units; later a byte far above them moves them, and O with them.
+  auto move_units = [&](uint32_t vw) {
+    int unit[4];
+    v_units(vadd[0], unit[0], unit[2]);
+    v_units(vadd[1], unit[1], unit[3]);
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n)
+    for (int b = 0; b < 4; ++b) {
+      const int high = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, (vw >> (8 * b)) & 0xFFu));
+      if (high <= unit[b] + kAttn4VAbove) continue;
+      const int down = unit[b] - high - kAttn4VRoom;
+      const float fv = down < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + down) << 23);
+      unit[b] -= down;
 #pragma unroll
-          for (int d = 0; d < 8; ++d)
+      for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][d][i] *= fv;
-      }
-      f02 <<= 10;
-      f13 <<= 10;
-      vfac_mine[0] = static_cast<uint16_t>(f02);
-      vfac_mine[2] = static_cast<uint16_t>(f13);
-      vfac_mine[4] = static_cast<uint16_t>(f02 >> 16);
-      vfac_mine[6] = static_cast<uint16_t>(f13 >> 16);
-      __syncwarp();
+        for (int d = 2 * b; d < 2 * b + 2; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][d][i] *= fv;
     }
-
-    // ---- S^T (two tiles of 16 keys): c0, c1: key attn4_key(g), c2, c3: 8 more; columns 2t, 2t + 1
-    float s[2][kTiles][4];
+    vadd[0] = v_addend(unit[0], unit[2]);
+    vadd[1] = v_addend(unit[1], unit[3]);
+  };
+  // S^T (two tiles of 16 keys): c0, c1: key attn4_key(g), c2, c3: 8 more; columns 2t, 2t + 1.
+  auto scores = [&](float (&s)[2][kTiles][4]) {
+    const uint8_t* kt = ring + st * kAttn4StageBytes;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r0 = 16 * h + attn4_key(g);
@@ -440,8 +527,9 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
         }
       }
     }
-
-    // ---- masks, running maximum (in log2 units: the factor is positive, so it can follow the maximum)
+  };
+  // Masks, running maximum (in log2 units: the factor is positive, so it can follow the maximum).
+  auto settle = [&](int tile, uint32_t gone, float (&s)[2][kTiles][4]) {
     if (gone != 0 || (tile + 1) * kAttn4Keys > lim_min) {
       const int key0 = tile * kAttn4Keys + attn4_key(g);
 #pragma unroll
@@ -475,7 +563,7 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
           m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
           const float f = mx[n][i] == -INFINITY ? 0.f : ex2_approx(mx[n][i] - m);  // no key yet: o and l are 0
           mx[n][i] = m;
-          off[n][i] = m == -INFINITY ? 0.f : kAttn4PBias - m;
+          off[n][i] = m == -INFINITY ? 0.f : static_cast<float>(kAttn4PBias) - m;
           l[n][i] *= f;
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
@@ -485,7 +573,49 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
         }
       }
     }
-    // ---- P^T as the B operand: 2^4 e^(s - m), keys 2t, 2t + 1 (and 8 more) of column g
+  };
+  auto advance = [&]() {
+    if (++st == kAttn4Stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  };
+
+  int tile = mine;
+#pragma unroll 1
+  for (; tile < tile1; tile += kAttn4Warps) {
+    if (!fetch(tile)) {
+      tile = tile1;
+      break;
+    }
+    const uint8_t* vt = ring + st * kAttn4StageBytes + 2048;
+    const uint32_t gone = (bad >> (2 * st)) & 3u;
+    {
+      bool there;
+      const uint32_t vw = scale_words(tile, gone, there);
+      // V: the place in the window of its scales, plus one, is the exponent field of an f16 factor. (A key that
+      // is not there has P = 0, and any factor; it is looked at only once the tile is.)
+      const uint32_t v02 = vw & 0x00FF00FFu, v13 = (vw >> 8) & 0x00FF00FFu;
+      uint32_t f02 = v02 + vadd[0], f13 = v13 + vadd[1];
+      const auto outside = [&]() { return __any_sync(0xFFFFFFFFu, ((f02 | f13) & 0xFFF0FFF0u) != 0u); };
+      if (outside()) {
+        move_units(vw);
+        f02 = there ? v02 + vadd[0] : 0u;
+        f13 = there ? v13 + vadd[1] : 0u;
+        if (outside()) break;
+      }
+      f02 = f02 * 1024u + 0x04000400u;
+      f13 = f13 * 1024u + 0x04000400u;
+      vfac_mine[0] = static_cast<uint16_t>(f02);
+      vfac_mine[2] = static_cast<uint16_t>(f13);
+      vfac_mine[4] = static_cast<uint16_t>(f02 >> 16);
+      vfac_mine[6] = static_cast<uint16_t>(f13 >> 16);
+      __syncwarp();
+    }
+    float s[2][kTiles][4];
+    scores(s);
+    settle(tile, gone, s);
+    // ---- P^T as the B operand: 2^10 e^(s - m), keys 2t, 2t + 1 (and 8 more) of column g
     uint32_t pb[2][kTiles][2];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
@@ -542,9 +672,22 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
         }
       }
     }
-    if (++st == kAttn4Stages) {
-      st = 0;
-      phase ^= 1u;
+    advance();
+  }
+  // From a tile with a scale outside the window on (its keys' scale words are in place).
+  if (tile < tile1) {
+#pragma unroll 1
+    for (;;) {
+      __syncwarp();
+      float s[2][kTiles][4];
+      scores(s);
+      settle(tile, (bad >> (2 * st)) & 3u, s);
+      attn4_wide<kTiles>(ring + st * kAttn4StageBytes, lane, vadd, s, c2, off, l, o);
+      advance();
+      tile += kAttn4Warps;
+      if (tile >= tile1 || !fetch(tile)) break;
+      bool there;
+      move_units(scale_words(tile, (bad >> (2 * st)) & 3u, there));
     }
   }
   __syncwarp();
@@ -553,7 +696,20 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
   // the cluster's. Rows that do not exist are left out.
   const int real = min(kRows, rows - row0);
   float* part = reinterpret_cast<float*>(ring);  // [kRows][kPitch], then m[kRows], l[kRows]
-  const int undo = static_cast<int>(vref) - 127 - kAttn4VBias;
+  // O is still in V's units and with both biases, l with P's: factors 2^(unit - 127 - biases) in two halves, each a
+  // normal number (without a tile there is no unit, and O is 0).
+  float undo[4][2];
+  {
+    int unit[4];
+    v_units(vadd[0], unit[0], unit[2]);
+    v_units(vadd[1], unit[1], unit[3]);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int e = max(-250, unit[b] - 127 - kAttn4VBias - kAttn4PBias);
+      undo[b][0] = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
+      undo[b][1] = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
+    }
+  }
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
@@ -565,13 +721,13 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
       if (row >= real) continue;
       if (g == 0) {
         part[kRows * kPitch + row] = mx[n][i];
-        part[kRows * kPitch + kRows + row] = l[n][i];
+        part[kRows * kPitch + kRows + row] = l[n][i] * (1.f / (1 << kAttn4PBias));
       }
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
         float* to = part + row * kPitch + 32 * (d >> 1) + 4 * g + 2 * (d & 1);
-        to[0] = scalbnf(o[n][d][i], undo);
-        to[1] = scalbnf(o[n][d][2 + i], undo);
+        to[0] = o[n][d][i] * undo[d >> 1][0] * undo[d >> 1][1];
+        to[1] = o[n][d][2 + i] * undo[d >> 1][0] * undo[d >> 1][1];
       }
     }
   }
@@ -608,9 +764,9 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     const int head = kvh * p.group + rr - tok * p.group;
     const float res = lsum == 0.f ? 0.f : acc / lsum;
     p.out[((q0 + static_cast<int64_t>(tok)) * p.heads_q + head) * 128 + ch] = __float2bfloat16(res);
-    if (ch == 0)  // l carries P's bias
+    if (ch == 0)
       p.lse[head * p.total_q + q0 + tok] =
-          lsum == 0.f ? -INFINITY : (m + lg2_approx(lsum) - kAttn4PBias) * 0.69314718055994531f;
+          lsum == 0.f ? -INFINITY : (m + lg2_approx(lsum)) * 0.69314718055994531f;
   };
   for (int row = threadIdx.x >> 7; row < real; row += kJoiners) {
     float ms[kAttn4Warps], ls[kAttn4Warps], os[kAttn4Warps], m, lsum, acc;
