@@ -561,12 +561,13 @@ LPFA_API lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_
  * Attention of a few query tokens per sequence over the MXFP4 cache (decoding; drafted tokens),
  * head-dim 128, q_heads a multiple of the cache's heads (query head h reads key head
  * h / (q_heads / heads)). Scale 1 / sqrt(128); the codes are exact, sums and softmax statistics are
- * FP32, and P is rounded to FP16's 11 bits, before or after its product with V's scale. Where V's scales of
- * a channel block (32 elements) lie within 11 binades of each other a product is off by at most 2^-35 of the
- * largest weight times the largest scale, and nowhere by more than 2^-20 of the row's largest product of a
- * weight and a scale of the block. What is 2^100 below the largest scale of its block may count as 0, and so may
- * elements of q below 2^-38 of the largest of their row. Any number of query tokens is right; the kernel reads the cache once
- * per 16 query rows, so long chunks are faster through lpfa_kv4_read and lpfa_attn_fwd_varlen.
+ * FP32, and P is rounded to FP16's 11 bits, before or after its product with V's scale. A product is off
+ * by at most 2^-20 of the row's largest product of a weight and a scale of the channel block (32 elements)
+ * besides, and by at most 2^-31 of its largest weight times the largest scale where V's scales of the block
+ * lie within 11 binades. What is 2^100 below the largest scale of its block may count as 0, and so may
+ * elements of q below 2^-38 of the largest of their row. Any number of query tokens is right; the kernel
+ * reads the cache once per 16 query rows, so long chunks are faster through lpfa_kv4_read and
+ * lpfa_attn_fwd_varlen.
  *
  * q          bf16 rows (Tq, q_heads, 128) under meta_q, strides in elements.
  * kv_lens    device, int32 per sequence: cached tokens, those of this step included; 0 is allowed.

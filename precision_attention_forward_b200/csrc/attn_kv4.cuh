@@ -26,8 +26,8 @@
 // takes from its first tile; the window of scales from 2^-15 to 2^0 of the unit becomes 2^-14 to 2^1, and the
 // product of both is at most 2^15. A weight keeps its 11 bits down to 2^-24 of the reference, and its product
 // down to 2^-25 of the largest that the window allows; below that a product is off by at most 2^-35 of the
-// largest weight times the largest scale: 2^-20 of the row's largest p 2^e (e: the scale) at worst, since the key of
-// the reference has a scale in the window too.
+// reference times the unit: 2^-20 of the row's largest p 2^e (e: the scale) at worst, since the key of the
+// reference has a scale in the window too.
 // With a scale outside the window neither holds: a large one that the row does not see or hardly weighs would take the
 // others' bits. From such a tile on, the warp joins P and V's scale in FP32 and rounds once, relative to the
 // tile's largest p 2^e in each row and channel block (attn4_wide). That costs up to 1.8 times the tame form:
@@ -36,8 +36,8 @@
 // S and the softmax statistics are FP32.
 //
 // Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and
-// accumulators (no barrier in the loop); one lane fetches the tiles ahead by bulk copies, two to six
-// for a tile (a page holds 16 tokens or more), into the warp's ring. What the lanes of a row or column
+// accumulators (no barrier in the loop); the tiles ahead come by bulk copies into the warp's ring, four for a
+// tile within one page, from one lane, and eight, from two, for the halves of a tile of 16-token pages. What the lanes of a row or column
 // share, they compute once: lane i turns key i's scale bytes into factors and leaves them in shared
 // memory. The blocks of a cluster share the keys of one (sequence, key head, query tile) and join
 // their partial results through distributed shared memory: one launch, no workspace, and always the
