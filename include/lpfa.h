@@ -548,8 +548,8 @@ LPFA_API lpfa_status lpfa_kv4_write(const lpfa_rows* k, const lpfa_rows* v, lpfa
 /*
  * The cached tokens start[i] .. start[i] + len_i of each sequence (len_i from meta) as packed MXFP8
  * tensors in the quantizer's layout, exactly: E2M1 codes are E4M3 values and the scales are the
- * same bytes. For a long chunk of queries over a cached prefix, through lpfa_attn_fwd_varlen (bf16
- * PV mode) or lpfa_dequantize_mxfp8_varlen. Rows past a sequence's end get scale bytes 0x7F.
+ * same bytes. For lpfa_attn_fwd_varlen (bf16 PV mode; noncausal, and q with the cache's heads, so not for
+ * grouped heads or a causal chunk) or lpfa_dequantize_mxfp8_varlen. Rows past a sequence's end get scale bytes 0x7F.
  * Errors as for lpfa_kv4_write.
  */
 LPFA_API lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* table,
@@ -565,9 +565,10 @@ LPFA_API lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_
  * by at most 2^-20 of the row's largest product of a weight and a scale of the channel block (32 elements)
  * besides, and by at most 2^-31 of its largest weight times the largest scale where V's scales of the block
  * lie within 11 binades. What is 2^100 below the largest scale of its block may count as 0, and so may
- * elements of q below 2^-38 of the largest of their row. Any number of query tokens is right; the kernel
- * reads the cache once per 16 query rows, so long chunks are faster through lpfa_kv4_read and
- * lpfa_attn_fwd_varlen.
+ * elements of q below 2^-38 of the largest of their row. Any number of query tokens is right, but
+ * every 8 or 16 query rows (tokens times query heads of a key head) read the cache again: chunks of many tokens
+ * with the cache's heads and no mask are faster through lpfa_kv4_read and lpfa_attn_fwd_varlen, which has
+ * neither grouped heads nor a causal mask.
  *
  * q          bf16 rows (Tq, q_heads, 128) under meta_q, strides in elements.
  * kv_lens    device, int32 per sequence: cached tokens, those of this step included; 0 is allowed.

@@ -300,6 +300,29 @@ def descale_strides(t: torch.Tensor, num_seqs: int, heads: int):
                      % (tuple(t.shape),))
 
 
+def _check_packed(q, q_sf, k, k_sf, v, v_sf, meta_q: "VarlenMeta", meta_k: "VarlenMeta", v_dtype) -> None:
+    """Q, K and V and their scale storage hold what the kernels will read of them: one head count for all
+    three, at least the metadata's tokens, and scales for their blocks. (A missing v_sf is the library's to refuse.)"""
+    H = q.shape[1] if q.dim() == 3 else 0
+    for name, t, meta, dtype in (("q", q, meta_q, torch.uint8), ("k", k, meta_k, torch.uint8), ("v", v, meta_k, v_dtype)):
+        if (t.dtype != dtype or t.dim() != 3 or t.shape[0] < meta.total_tokens or t.shape[1] != H or t.shape[2] != 128
+                or not t.is_contiguous() or t.device != q.device):
+            raise ValueError("%s must be a contiguous %s (tokens, heads, 128) tensor on the device of q with the %d tokens "
+                             "of its metadata and q's %d heads, not %s" % (name, dtype, meta.total_tokens, H, tuple(t.shape)))
+    for name, t, meta in (("q_sf", q_sf, meta_q), ("k_sf", k_sf, meta_k), ("v_sf", v_sf, meta_k)):
+        if t is None and name == "v_sf":
+            continue
+        if t.numel() * t.element_size() < meta.scale_bytes(H) or not t.is_contiguous() or t.device != q.device:
+            raise ValueError("%s must hold %d contiguous scale bytes on the device of q" % (name, meta.scale_bytes(H)))
+
+
+def _check_out_lse(out, lse, rows: int, heads: int, device) -> None:
+    """Given outputs of the forward (None: allocated) hold what it writes."""
+    for name, t, dtype, shape in (("out", out, torch.bfloat16, (rows, heads, 128)), ("lse", lse, torch.float32, (heads, rows))):
+        if t is not None and (t.dtype != dtype or t.numel() < np.prod(shape) or not t.is_contiguous() or t.device != device):
+            raise ValueError("%s must be a contiguous %s tensor of shape %s on the device of q" % (name, dtype, shape))
+
+
 def lpfa_attn_fwd_varlen(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor, k_sf: torch.Tensor,
                          v: torch.Tensor, v_sf: Optional[torch.Tensor], meta_q: VarlenMeta, meta_k: VarlenMeta,
                          pv_mode: str = "bf16", q_descale: Optional[torch.Tensor] = None,
@@ -308,6 +331,7 @@ def lpfa_attn_fwd_varlen(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor, k
                          debug_flags: int = 0, workspace=True):
     """Block-scaled attention forward; returns (out bf16 (Tq,H,128), lse fp32 (H,Tq)).
 
+    Every query sees every key of its sequence; Q, K and V have the same heads.
     q/k/v_descale: None (exactly 1.0), a one-element tensor (per tensor), (H,) (per head) or
     (S, H) (per sequence and head), float32 on the device; see descale_strides.
     workspace: where the bf16 PV mode converts V to BF16 once (lpfa_attn_fwd_varlen_ws): True
@@ -320,11 +344,10 @@ def lpfa_attn_fwd_varlen(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor, k
     """
     if pv_mode not in PV_MODES:
         raise ValueError("pv_mode must be 'bf16', 'fp8', 'bf16v' or 'mxfp8'")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        want = torch.bfloat16 if (name == "v" and pv_mode == "bf16v") else torch.uint8
-        if t.dtype != want or t.dim() != 3 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s (tokens, heads, 128) tensor" % (name, want))
+    _check_packed(q, q_sf, k, k_sf, v, v_sf if pv_mode in ("bf16", "mxfp8") else None, meta_q, meta_k,
+                  torch.bfloat16 if pv_mode == "bf16v" else torch.uint8)
     Tq, H = q.shape[0], q.shape[1]
+    _check_out_lse(out, lse, meta_q.total_tokens, H, q.device)
     descs = []
     for name, t in (("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale)):
         if t is None:
@@ -410,10 +433,8 @@ def lpfa_attn_fwd_shared_q(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor,
         raise ValueError("pv_mode must be 'bf16', 'fp8', 'bf16v' or 'mxfp8'")
     if meta_q.num_seqs != 1:
         raise ValueError("a shared query set is one sequence")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        want = torch.bfloat16 if (name == "v" and pv_mode == "bf16v") else torch.uint8
-        if t.dtype != want or t.dim() != 3 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s (tokens, heads, 128) tensor" % (name, want))
+    _check_packed(q, q_sf, k, k_sf, v, v_sf if pv_mode in ("bf16", "mxfp8") else None, meta_q, meta_k,
+                  torch.bfloat16 if pv_mode == "bf16v" else torch.uint8)
     Lq, H = q.shape[0], q.shape[1]
     rows = Lq * meta_k.num_seqs
     descs = []
@@ -431,6 +452,7 @@ def lpfa_attn_fwd_shared_q(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor,
         lse = torch.empty((H, rows), dtype=torch.float32, device=q.device)
     if tuple(out.shape) != (rows, H, 128) or tuple(lse.shape) != (H, rows):
         raise ValueError("out must be (n*Lq, H, 128) and lse (H, n*Lq)")
+    _check_out_lse(out, lse, rows, H, q.device)
     ws = _workspace(workspace, meta_k, H, pv_mode, q.device, stream)
     args = (q.data_ptr(), q_sf.data_ptr(), k.data_ptr(), k_sf.data_ptr(), v.data_ptr(), _ptr(v_sf),
             ctypes.byref(meta_q._c), ctypes.byref(meta_k._c), H, 128, PV_MODES[pv_mode], ctypes.byref(descs[0]),
@@ -458,9 +480,7 @@ def lpfa_attn_bwd_varlen(q: torch.Tensor, q_sf: torch.Tensor, k: torch.Tensor, k
     Output tensors may be passed in (contiguous, of the returned shapes and dtypes); debug_flags != 0
     calls the test hook lpfa_attn_bwd_varlen_debug.
     """
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous uint8 (tokens, heads, 128) tensor" % name)
+    _check_packed(q, q_sf, k, k_sf, v, v_sf, meta_q, meta_k, torch.uint8)
     for name, t in (("out", out), ("dout", dout)):
         if t.dtype != torch.bfloat16 or t.shape != q.shape or not t.is_contiguous():
             raise ValueError("%s must be a contiguous bf16 tensor shaped like q" % name)
@@ -931,8 +951,8 @@ def lpfa_kv4_read(cache: Kv4Cache, page_table: torch.Tensor, meta: VarlenMeta, s
                   k_payload: Optional[torch.Tensor] = None, k_scales: Optional[torch.Tensor] = None,
                   v_payload: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None, stream=None):
     """The cached tokens start[i] .. start[i] + length_i (lengths from meta) as packed MXFP8 tensors,
-    exactly: (k_payload, k_scales, v_payload, v_scales) in the quantizer's layout, for
-    lpfa_attn_fwd_varlen (pv_mode "bf16") or lpfa_dequantize_mxfp8_varlen."""
+    exactly: (k_payload, k_scales, v_payload, v_scales) in the quantizer's layout, for lpfa_attn_fwd_varlen
+    (pv_mode "bf16"; without a mask, and Q with the cache's heads) or lpfa_dequantize_mxfp8_varlen."""
     device = cache.device
     _check_meta_device(meta, device)
     num_seqs = meta.num_seqs
@@ -959,7 +979,9 @@ def lpfa_attn_fwd_kv4(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor
     q: bf16 (Tq, q_heads, 128), q_heads a multiple of the cache's heads, packed under meta_q. kv_lens:
     int32 per sequence, the cached tokens (this step's included; 0 gives O = 0, LSE = -inf). causal:
     query token j of L sees the first kv_lens - L + j + 1 keys, else all of them. The page table is as
-    for lpfa_kv4_write. For chunks of many query tokens, lpfa_kv4_read and lpfa_attn_fwd_varlen are faster.
+    for lpfa_kv4_write. Any number of query tokens is right, but every 8 or 16 query rows (tokens times query
+    heads of a key head) read the cache again. Chunks of a few hundred tokens with as many heads as the cache and no
+    causal mask are faster through lpfa_kv4_read and lpfa_attn_fwd_varlen, which has neither grouped heads nor a mask.
     """
     device = cache.device
     index = device.index
