@@ -68,7 +68,8 @@ constexpr int kAttn4VFactors = kAttn4KFactors + kAttn4Keys * 16;
 constexpr int kAttn4Bars = kAttn4VFactors + kAttn4Keys * 8;
 constexpr int kAttn4Ring = kAttn4Bars + 16 * ((kAttn4Stages + 1) / 2);
 constexpr int kAttn4MaxSplit = 16;  // blocks of a cluster
-constexpr int kAttn4SortMax = 512;  // sequences that are put in order
+constexpr int kAttn4SortRounds = 4;  // rounds of blocks up to which the sequences are put in order
+constexpr int kAttn4SortKeys = 1024;  // keys of the longest one from which on they are
 constexpr float kAttn4Lag = 4.f;    // binades that the running maximum may be exceeded by
 constexpr int kAttn4PBias = 10;     // P is 2^10 e^(s - m), at most 2^14
 constexpr int kAttn4VBias = 1;      // V's scale is 2^(1 + byte - unit), at most 2^1
@@ -238,6 +239,61 @@ __device__ __forceinline__ void attn4_wide(const uint8_t* kt, int lane, const ui
   }
 }
 
+// Sequence number `nth` of the lengths in falling order, to a 64th of the longest, and equals by their number; where
+// all are short, just number `nth`. Every block works it out for itself, since the lengths are on the device only,
+// with work in proportion to their number, about 1 us a block for a few hundred. All threads take part; `mem`
+// holds 64 + 2 kWarps words.
+template <int kWarps>
+__device__ __forceinline__ int attn4_nth_longest(const int32_t* lens, int n, int nth, int32_t* mem) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t *count = mem, *tops = mem + 64, *found = tops + kWarps;
+  int top = 1;
+  for (int i = threadIdx.x; i < n; i += 32 * kWarps) top = max(top, __ldg(lens + i));
+  top = __reduce_max_sync(kAll, top);
+  if (lane == 0) tops[warp] = top;
+  if (threadIdx.x < 64) count[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, tops[w]);
+  if (top < kAttn4SortKeys) return nth;
+  const float scale = 63.5f / static_cast<float>(top);
+  auto bucket = [&](int i) { return 63 - static_cast<int>(scale * static_cast<float>(max(0, __ldg(lens + i)))); };
+  for (int i = threadIdx.x; i < n; i += 32 * kWarps) atomicAdd(&count[bucket(i)], 1);
+  __syncthreads();
+  // The bucket that holds number nth, and its number there: lane's two buckets start at number `before`.
+  const int c0 = count[2 * lane], c1 = count[2 * lane + 1];
+  int before = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(kAll, before, d);
+    if (lane >= d) before += up;
+  }
+  before -= c0 + c1;
+  const int owner = 31 - __clz(__ballot_sync(kAll, before <= nth));
+  const int second = nth >= before + c0;
+  const int mine = __shfl_sync(kAll, 2 * lane + second, owner);
+  int left = nth - __shfl_sync(kAll, before + (second ? c0 : 0), owner);
+  // Each warp counts the bucket's members in a part of the sequences; then the part that has it is gone through.
+  const int part = (n + 32 * kWarps - 1) / (32 * kWarps) * 32;
+  int members = 0;
+  for (int i = warp * part; i < min(n, (warp + 1) * part); i += 32)
+    members += __popc(__ballot_sync(kAll, i + lane < n && bucket(i + lane) == mine));
+  if (lane == 0) found[warp] = members;
+  __syncthreads();
+  int at = 0;
+  for (; at < kWarps - 1 && left >= found[at]; ++at) left -= found[at];
+  for (int i = at * part;; i += 32) {
+    const uint32_t in = __ballot_sync(kAll, i + lane < n && bucket(i + lane) == mine);
+    if (left >= __popc(in) && i + 32 < n) {
+      left -= __popc(in);
+      continue;
+    }
+    const uint32_t it = __ballot_sync(kAll, ((in >> lane) & 1u) && __popc(in & ((1u << lane) - 1u)) == left);
+    return max(0, i + __ffs(it) - 1);
+  }
+}
+
 // kTiles: tiles of 8 query rows that a block holds (rows = query tokens x query heads of a key head).
 template <int kTiles>
 __global__ void __launch_bounds__(32 * attn4_warps<kTiles>(), kTiles == 1 ? 16 / attn4_warps<kTiles>() : 2)
@@ -259,20 +315,8 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
   const int kvh = w % p.c.heads;
   int seq = w / p.c.heads;
   if (p.sorted) {
-    // Longest sequences first, so that the last blocks to run are short ones: sequence number `seq` of
-    // that order. Every block works it out for itself (the lengths are on the device only).
-    int32_t* lens = reinterpret_cast<int32_t*>(smem4);
-    int32_t* nth = lens + kAttn4SortMax;
-    for (int i = threadIdx.x; i < p.num_seqs; i += kAttn4Threads) lens[i] = __ldg(p.kv_lens + i);
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.num_seqs; i += kAttn4Threads) {
-      const int mine = lens[i];
-      int rank = 0;
-      for (int k = 0; k < p.num_seqs; ++k) rank += lens[k] > mine || (lens[k] == mine && k < i);
-      if (rank == seq) *nth = i;
-    }
-    __syncthreads();
-    seq = *nth;
+    // Longest sequences first, so that the last blocks to run are short ones.
+    seq = attn4_nth_longest<kAttn4Warps>(p.kv_lens, p.num_seqs, seq, reinterpret_cast<int32_t*>(smem4));
     __syncthreads();  // the rings come next in this memory
   }
   const int q0 = __ldg(p.cu_q + seq);

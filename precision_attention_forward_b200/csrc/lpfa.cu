@@ -1243,9 +1243,10 @@ lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, int
     cfg.gridDim = dim3(static_cast<unsigned>(work * p.splits));
     if (p.splits <= 8 || attn4_clusters<kTiles>(cfg, dev, p.splits) >= work) break;
   }
-  // Blocks that have to wait for others' places run in order of length (64 ragged sequences of up to
-  // 8192 keys: 80 instead of 106 us).
-  p.sorted = p.num_seqs > 1 && p.num_seqs <= lpfa::kAttn4SortMax && work * p.splits > 2 * sms;
+  // Blocks that have to wait for others' places run in order of length, where there are few rounds of them and the
+  // order matters more than its cost (8 key heads, with and without: 64 ragged sequences of up to 8192 keys
+  // 70 and 99 us, 128 of 2000 53 and 56; 256 of 2000, 7 rounds, 100 either way, 512 of 300 110 and 92).
+  p.sorted = p.num_seqs > 1 && work * p.splits > 2 * sms && work * p.splits <= 2 * sms * lpfa::kAttn4SortRounds;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache attention launch");
 }
