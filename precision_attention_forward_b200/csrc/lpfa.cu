@@ -1181,12 +1181,14 @@ lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_table* ta
   int dev = 0;
   if ((st = require_sm100(&info, &dev)) != LPFA_OK) return st;
   const dim3 grid(static_cast<unsigned>(meta->total_scale_blocks) * 4u, 2);
-  const int smem = cache->heads * lpfa::kKv4Tile * 4;  // up to 128 KB
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(lpfa::kv4_read_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  // The limit is the kernel's largest need, not this call's: another thread may be about to launch with more heads.
+  static KernelLimits limits;
+  constexpr int kMost = kMaxRopeHeads * lpfa::kKv4Tile * 4;  // 128 KB
+  st = set_limits(limits, reinterpret_cast<const void*>(lpfa::kv4_read_kernel), dev, kMost, false);
+  if (st != LPFA_OK) return st;
+  const int smem = cache->heads * lpfa::kKv4Tile * 4;
   lpfa::kv4_read_kernel<<<grid, lpfa::kKv4Threads, static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)>>>(p);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LPFA_OK : cuda_fail(e, "cache read launch");
 }
 
