@@ -545,8 +545,6 @@ class _Scope:
         self.other = stream
 
     def __enter__(self):
-        if self.restore is not None:
-            self.restore.__enter__()
         self.handle = torch._C._cuda_getCurrentRawStream(self.device.index)
         if self.other is not None:
             stream = self.other
@@ -556,8 +554,10 @@ class _Scope:
                 raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
             self.other = None
             if stream.cuda_stream != self.handle:
-                self.caller = torch.cuda.current_stream()
+                self.caller = torch.cuda.current_stream(self.device)
                 self.handle, self.other = stream.cuda_stream, stream
+        if self.restore is not None:  # last: what is refused above leaves the current device alone
+            self.restore.__enter__()
         return self
 
     def __exit__(self, *exc):
