@@ -5,6 +5,10 @@ Argument marshalling only: every step of the path runs in the library's CUDA ker
 (``liblpfa.so``, built in-tree for sm_100a). PyTorch provides device memory and streams.
 Importing this package fails if the library has not been built; there is no CPU fallback.
 
+Every function that takes `stream` enqueues its work there (None: the current stream) and returns without waiting.
+With another stream than the current one, the caller orders it behind the work that made the inputs, and keeps the
+tensors that it hands in alive, or recorded on that stream, until the work is done.
+
 The functions carry the C ABI's names (``include/lpfa.h``); the LP-FA4 README names
 (``Mxfp8VarlenMeta.from_lengths``, ``quantize_mxfp8_varlen``,
 ``mxfp8_flash_attn_varlen_forward``) are provided as aliases.
@@ -742,7 +746,8 @@ def lpfa_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Opt
     their head counts may differ and k may be None. positions: (tokens, axes) int32 or int64, or
     (tokens,) for one axis. rope: a RotaryAxes, or None for no rotation. q_weight, k_weight: (128,) or
     (heads, 128), bf16 or fp32. norm=False leaves the norm out (the weight still applies).
-    Outputs: out_dtype (the input's by default), contiguous unless given; an output may be its own input.
+    Outputs: out_dtype (the input's by default), contiguous unless given; an output may be its own input, of the same
+    type and strides, and overlaps nothing else.
     """
     index = q.get_device()
     qr, kr, k_heads = _qk_rows(q, k, index)
@@ -886,6 +891,12 @@ class Kv4Cache:
         self._set(k, k_scales, v, v_scales)
         return self
 
+    # Not to be replaced: the calls use the addresses taken here.
+    k = property(lambda self: self._tensors[0])
+    k_scales = property(lambda self: self._tensors[1])
+    v = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+
     def _set(self, k, k_scales, v, v_scales):
         if k.dim() != 4 or k.shape[3] != 64 or k.shape[2] not in (16, 32, 64, 128, 256):
             raise ValueError("k must be (num_pages, heads, page_size, 64) with 16, 32, 64, 128 or 256 tokens per page")
@@ -893,7 +904,7 @@ class Kv4Cache:
             raise ValueError("the cache lives on a CUDA device")
         for name, t, n in (("k", k, 64), ("k_scales", k_scales, 4), ("v", v, 64), ("v_scales", v_scales, 4)):
             _contiguous(t, name, torch.uint8, k.device, tuple(k.shape[:3]) + (n,))
-        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self._tensors = (k, k_scales, v, v_scales)
         self.num_pages, self.heads, self.page_size = k.shape[0], k.shape[1], k.shape[2]
         self.device = k.device
         self._c = _Kv4Cache(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), *k.shape[:3])

@@ -87,3 +87,15 @@ def test_writes_and_attention_at_a_time():
     for w, x in zip(want, got):
         assert torch.equal(w[0], x[0]) and torch.equal(w[1], x[1])
     assert lp.lpfa_device_status() == (lp.LPFA_OK, 0)
+
+
+def test_a_cache_keeps_the_tensors_that_its_calls_write_to():
+    """The handle holds addresses: its tensors are its own for good, and a new pool is a new handle."""
+    cache = lp.Kv4Cache(2, 1, 16)
+    for name in ("k", "k_scales", "v", "v_scales"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros_like(getattr(cache, name)))
+    same = lp.Kv4Cache.from_tensors(cache.k, cache.k_scales, cache.v, cache.v_scales)
+    x = torch.randn(5, 1, 128, device="cuda").bfloat16()
+    lp.lpfa_kv4_write(x, x, same, torch.ones(1, 1, dtype=torch.int32, device="cuda"), lp.lpfa_varlen_meta_from_lengths([5]))
+    assert cache.k[1, 0, :5].any() and not cache.k[0].any() and torch.equal(cache.k, cache.v)
