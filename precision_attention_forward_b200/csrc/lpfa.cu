@@ -1235,7 +1235,7 @@ lpfa_status launch_attn_kv4(lpfa::Attn4Params& p, int64_t max_rows, int sms, int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // As many blocks as run at a time, two per SM, but 128 keys for each at least. (Two rounds of half
-  // as long blocks took 35 instead of 25 us for 8 x 5 query tokens over 4096 keys.) Clusters beyond
+  // as long blocks take 27 instead of 16 us for 8 x 5 query tokens over up to 4096 keys.) Clusters beyond
   // the portable size of 8 only where the device can place all of them at once.
   const int64_t keys = static_cast<int64_t>(p.c.width) << p.c.page_shift;
   p.splits = static_cast<int>(
@@ -1290,8 +1290,10 @@ lpfa_status lpfa_attn_fwd_kv4(const lpfa_rows* q, int32_t head_dim, const lpfa_k
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // One row costs what eight do. Sixteen per block cost 5/3 as much as eight (conversions and reads of the
   // cache are shared) with half as many warps on an SM: taken where that is less work for the longest
-  // sequence's rows, and where the largest split still fills the card. (16 rows: 32 x 8192 keys 65
-  // instead of 80 us, but 4 x 65536 keys 116 instead of 74; 20 rows of 8 x 4096 keys 23 instead of 20.)
+  // sequence's rows, and where the largest split still fills the card. (16 rows over 8 key heads: 32 x 8192
+  // keys 105 instead of 143 us; where the split would not fill it, 1 x 65536 58 instead of 50 and 4 x 2048
+  // 14.4 instead of 12.8, though 4 x 65536 106 instead of 138; 20 rows over 4 heads of 8 x 4096 keys 19
+  // instead of 17.)
   const int64_t tiles16 = (max_rows + 15) / 16, tiles8 = (max_rows + 7) / 8;
   const bool sixteen = 5 * tiles16 < 3 * tiles8 && tiles16 * p.c.heads * p.num_seqs * 8 >= 2 * info.sms;
   return sixteen ? launch_attn_kv4<2>(p, max_rows, info.sms, dev, s) : launch_attn_kv4<1>(p, max_rows, info.sms, dev, s);

@@ -19,9 +19,10 @@
 // angles depend on the token alone: a warp computes its token's once. An angle is a product in FP64
 // reduced by one FMA to a rest of at most an eighth of a turn (exact up to the frequency's own
 // rounding), so far positions keep their accuracy, and short series do the rest.
-// Measured (B200): that case 126 us, the time of a device copy of its bytes; 8192 tokens x 32 heads of
-// BF16 into MXFP8 29 us, where 270 warp instructions a step bound it (4 rows: norm and rotation 150,
-// block maxima, scale bytes and conversion 120); ragged FP32 sequences into MXFP8 at 95 % of the copy
+// Measured (B200): that case 127 us, the time of a device copy of its bytes; 8192 tokens x 32 heads of
+// BF16 into MXFP8 29 us, bound by the latency of shuffles and conversions at 16 warps an SM: its 270 warp
+// instructions a step (4 rows: norm and rotation 150, block maxima, scale bytes and conversion 120) take 56 % of
+// the issue slots; ragged FP32 sequences into MXFP8 at 95 % of the copy
 // bandwidth, and at 85 % once the power limit has lowered the clock.
 #pragma once
 
@@ -39,8 +40,8 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeTokens = 4 * kRopeWarps;  // tokens of a forward block, at most
 constexpr int kRopeBatch = 2;                // forward steps that a warp takes together
 // Batches of a warp's shared-memory ring (2 KB each for BF16 input, 4 KB for FP32): one computed, one on
-// the way. More of them are slower: with four (three) the video forward took 151 instead of 132 us and
-// the ragged FP32 to MXFP8 one 272 instead of 258, since the warps' tokens lie apart in memory and
+// the way. More of them are slower: with four (three) the video forward took 151 us when it took 132 with two,
+// and the ragged FP32 to MXFP8 one 272 against 258, since the warps' tokens lie apart in memory and
 // each keeps more places of it open.
 template <typename T> constexpr int rope_stages() { return 2; }
 template <typename T> constexpr int rope_stage_bytes() { return kRopeBatch * 4 * 128 * static_cast<int>(sizeof(T)); }
@@ -403,7 +404,7 @@ __device__ __forceinline__ void make_turn(Turn& m, const float* cs, const Pairs&
 // of the atoms between them. The warps are on their own, without a barrier: each computes its tokens'
 // angles while its first rows are on the way, and loads ahead into its next token. (The other mapping, in
 // which a block's warps share each token's rows and sweep contiguous memory, needs a barrier and an
-// address calculation per item: 167 us for the case that takes 132.)
+// address calculation per item: 167 us when the video forward took 132.)
 template <typename TIn, int kOut, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 qk_norm_rope_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ RopePlan plan) {
@@ -784,9 +785,9 @@ __device__ __forceinline__ void rope_bwd_angles(const RopeParams& p, const LaneT
   __syncthreads();
 }
 
-// Backward with at most one weight row for all heads (8192 tokens x 32 heads of BF16: 43.4 us with the
-// sums, 1.4 times the copy time of its bytes; 92 warp instructions a row and the three-shuffle sums
-// bound it). Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step (four
+// Backward with at most one weight row for all heads (8192 tokens x 32 heads of BF16: 43.5 us with the
+// sums, 1.4 times the copy time of its bytes, bound by the latency of two sums of three shuffles a row and
+// the reads of the angles at 16 warps an SM; its 92 warp instructions a row are half of the issue slots). Each block walks `tile` consecutive tokens, kRopeBwdTile at a time, in items of one step (four
 // rows, as in the forward pass) that go round the warps, each with the next one on the way in its
 // shared-memory ring. A lane's sums for its 16 channels stay in registers to the end. No atomics: the same
 // sums in the same order every time.
