@@ -564,7 +564,7 @@ LPFA_API lpfa_status lpfa_kv4_read(const lpfa_kv4_cache* cache, const lpfa_page_
  * FP32, and P is rounded to FP16's 11 bits, before or after its product with V's scale. A product is off
  * by at most 2^-20 of the row's largest product of a weight and a scale of the channel block (32 elements)
  * besides, and by at most 2^-31 of its largest weight times the largest scale where V's scales of the block
- * lie within 11 binades. What is 2^100 below the largest scale of its block may count as 0, and so may
+ * lie within 11 binades. What is 2^100 below the largest scale of its block in the sequence may count as 0, and so may
  * elements of q below 2^-38 of the largest of their row. Any number of query tokens is right, but
  * every 8 or 16 query rows (tokens times query heads of a key head) read the cache again: chunks of many tokens
  * with the cache's heads and no mask are faster through lpfa_kv4_read and lpfa_attn_fwd_varlen, which has

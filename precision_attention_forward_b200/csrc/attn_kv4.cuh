@@ -497,16 +497,16 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
       mbar_wait(&bars[(st + k) % kAttn4Stages], phase ^ (st + k >= kAttn4Stages ? 1u : 0u), nullptr);
     return false;
   };
-  // Scale words of key `lane` (K's as factors into shared memory: 2^e as floats; byte 0, 2^-127, counts as 0). Keys
-  // beyond hi or without a page have K's scales 0.
-  auto scale_words = [&](int tile, uint32_t gone, bool& there) {
+  // Scale words of key `lane`, K's as factors into shared memory (2^e as floats; byte 0, 2^-127, counts as 0). Those of
+  // a key beyond hi or without a page may be anything: its scores are masked.
+  auto scale_words = [&]() {
     const uint8_t* kt = ring + st * kAttn4StageBytes;
-    there = tile * kAttn4Keys + lane < hi && !((gone >> (lane >> 4)) & 1u);
-    const uint32_t kw = there ? *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane) : 0u;
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(kt + 4096 + 4 * lane);
     kfac[lane] = make_float4(__uint_as_float((kw << 23) & 0x7F800000u), __uint_as_float((kw << 15) & 0x7F800000u),
                              __uint_as_float((kw << 7) & 0x7F800000u), __uint_as_float((kw >> 1) & 0x7F800000u));
-    return there ? *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane) : 0u;
+    return *reinterpret_cast<const uint32_t*>(kt + 4224 + 4 * lane);
   };
+  auto is_there = [&](int tile) { return tile * kAttn4Keys + lane < hi && !((bad >> (2 * st + (lane >> 4))) & 1u); };
   // The first tile sets V's units; later a byte far above them moves them, and O with them.
   auto move_units = [&](uint32_t vw) {
     int unit[4];
@@ -635,15 +635,15 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
     const uint8_t* vt = ring + st * kAttn4StageBytes + 2048;
     const uint32_t gone = (bad >> (2 * st)) & 3u;
     {
-      bool there;
-      const uint32_t vw = scale_words(tile, gone, there);
+      const uint32_t vw = scale_words();
       // V: the place in the window of its scales, plus one, is the exponent field of an f16 factor. (A key that
-      // is not there has P = 0, and any factor; it is looked at only once the tile is.)
+      // is not there has P = 0, and any factor that is finite.)
       const uint32_t v02 = vw & 0x00FF00FFu, v13 = (vw >> 8) & 0x00FF00FFu;
       uint32_t f02 = v02 + vadd[0], f13 = v13 + vadd[1];
       const auto outside = [&]() { return __any_sync(0xFFFFFFFFu, ((f02 | f13) & 0xFFF0FFF0u) != 0u); };
       if (outside()) {
-        move_units(vw);
+        const bool there = is_there(tile);
+        move_units(there ? vw : 0u);
         f02 = there ? v02 + vadd[0] : 0u;
         f13 = there ? v13 + vadd[1] : 0u;
         if (outside()) break;
@@ -730,8 +730,8 @@ attn_kv4_kernel(const __grid_constant__ Attn4Params p) {
       advance();
       tile += kAttn4Warps;
       if (tile >= tile1 || !fetch(tile)) break;
-      bool there;
-      move_units(scale_words(tile, (bad >> (2 * st)) & 3u, there));
+      const uint32_t vw = scale_words();
+      move_units(is_there(tile) ? vw : 0u);
     }
   }
   __syncwarp();
