@@ -22,26 +22,26 @@
 // V's scale multiplies P (8 half2 products per 16 keys) and V's codes stay unscaled.
 //
 // Range. P is FP16 with the bias 2^10, relative to a reference that trails the maximum by at most 2^4. V's
-// scale is an FP16 power of two relative to a unit, one for each of the four channel blocks, which the warp
-// takes from its first tile; the window of scales from 2^-15 to 2^0 of the unit becomes 2^-14 to 2^1, and the
-// product of both is at most 2^15. A weight keeps its 11 bits down to 2^-24 of the reference, and its product
-// down to 2^-25 of the largest that the window allows; below that a product is off by at most 2^-35 of the
-// reference times the unit: 2^-20 of the row's largest p 2^e (e: the scale) at worst, since the key of the
-// reference has a scale in the window too.
-// With a scale outside the window neither holds: a large one that the row does not see or hardly weighs would take the
-// others' bits. From such a tile on, the warp joins P and V's scale in FP32 and rounds once, relative to the
-// tile's largest p 2^e in each row and channel block (attn4_wide). That costs up to 1.8 times the tame form:
-// 64 ragged sequences of up to 8192 keys with scales over 30 binades at random take 118 instead of 69 us.
-// O is FP32 in the block's unit, with room for 2^60 above it, where the unit moves, and 2^100 below.
-// S and the softmax statistics are FP32.
+// scale is an FP16 power of two relative to a unit, one for each of the four channel blocks, which the
+// warp takes from its first tile; the window of scales from 2^-15 to 2^0 of the unit becomes 2^-14 to 2^1,
+// and the product of both is at most 2^15. A weight keeps its 11 bits down to 2^-24 of the reference, and
+// its product down to 2^-25 of the largest that the window allows; below that a product is off by at most
+// 2^-35 of the reference times the unit: 2^-20 of the row's largest p 2^e (e: the scale) at worst, since
+// the key of the reference has a scale in the window too. With a scale outside the window neither holds: a
+// large one that the row does not see or hardly weighs would take the others' bits. From such a tile on,
+// the warp joins P and V's scale in FP32 and rounds once, relative to the tile's largest p 2^e in each row
+// and channel block (attn4_wide). That costs up to 1.8 times the tame form: 64 ragged sequences of up to
+// 8192 keys with scales over 30 binades at random take 118 instead of 69 us. O is FP32 in the block's
+// unit, with room for 2^60 above it, where the unit moves, and 2^100 below. S and the softmax statistics
+// are FP32.
 //
-// Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and
-// accumulators (no barrier in the loop); the tiles ahead come by bulk copies into the warp's ring, four for a
-// tile within one page, from one lane, and eight, from two, for the halves of a tile of 16-token pages. What the lanes of a row or column
-// share, they compute once: lane i turns key i's scale bytes into factors and leaves them in shared
-// memory. The blocks of a cluster share the keys of one (sequence, key head, query tile) and join
-// their partial results through distributed shared memory: one launch, no workspace, and always the
-// same order of sums.
+// Split. Each warp of a block walks its own tiles of 32 keys with its own running maximum and accumulators
+// (no barrier in the loop); the tiles ahead come by bulk copies into the warp's ring, four for a tile
+// within one page, from one lane, and eight, from two, for the halves of a tile of 16-token pages. What
+// the lanes of a row or column share, they compute once: lane i turns key i's scale bytes into factors and
+// leaves them in shared memory. The blocks of a cluster share the keys of one (sequence, key head, query
+// tile) and join their partial results through distributed shared memory: one launch, no workspace, and
+// always the same order of sums.
 #pragma once
 
 #include <cstdint>
